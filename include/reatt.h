@@ -77,7 +77,9 @@ typedef enum {
     REATT_EINVAL = 1,       /* null/misaligned pointer, bad or inconsistent size  */
     REATT_EUNSUPPORTED = 2, /* valid request outside what the kernels implement    */
     REATT_ECUDA = 3,        /* a CUDA call or kernel launch failed                  */
-    REATT_ETIMEOUT = 4      /* a kernel's bounded wait gave up (workspace status)   */
+    REATT_ETIMEOUT = 4,     /* a kernel's bounded wait gave up (workspace status)   */
+    REATT_EPAGE = 5         /* a page id or length out of range was left out
+                               (workspace status; paged calls only)                 */
 } reatt_status;
 
 typedef enum { REATT_F32 = 0, REATT_BF16 = 1 } reatt_dtype;
@@ -304,6 +306,104 @@ REATT_API int reatt_shard_attend(const reatt_dims *dims, const reatt_shard *shar
 REATT_API int reatt_merge_partials(const reatt_dims *dims, int32_t n_parts,
                                    const void *part_ml_all, const float *part_acc_all,
                                    float *out, reatt_stream stream);
+
+/* ---------------------------------------------------------------------------
+ * Many sequences of different lengths whose whole context is attended: a
+ * paged key-value cache and packed prompts.
+ *
+ * reatt_step serves one long un-rotated cache through a finite window.  While
+ * a sequence still fits that window (T + C <= G + k*S + L + C) the method is
+ * ordinary causal RoPE attention over everything cached; these calls serve
+ * that case for a batch of sequences that share a pool of pages.
+ *
+ * Layouts (dtype = dims->dtype; int32 arrays on the device)
+ *   packed rows    q [N, Hq, d], k/v [N, Hkv, d]: the new tokens of all
+ *                  sequences one after the other.  Rows may lie further apart
+ *                  than dense (q_stride ... in elements, 0 = dense, multiples
+ *                  of 16 bytes), so q, k and v may be slices of one projection.
+ *   cu_seqlens     [B + 1]: sequence b holds packed rows [cu[b], cu[b+1]);
+ *                  ascending, sequences may be empty; rows before cu[0] and
+ *                  from cu[B] on belong to no sequence and are left as they are
+ *   k/v_pages      [n_pages, Hkv, page, d]
+ *   page_table     [B, max_pages]: token t of sequence b is in slot t % page
+ *                  of page page_table[b, t / page]; entries past a sequence's
+ *                  tokens are not read
+ * Two sequences may share a page that is only read; a page that a call writes
+ * belongs to one sequence.  Outputs must not overlap inputs (except q_rot == q
+ * and k_rot == k).  No call waits for the host, so all of them can be captured
+ * into a CUDA graph; lengths and tables are read when the kernel runs.
+ *
+ * A page id outside [0, n_pages), or a length outside [0, max_pages * page],
+ * never leads out of the pools: such tokens are left out (lengths are clamped)
+ * and REATT_EPAGE is recorded in the workspace status word; the results of that
+ * sequence are then unspecified.
+ * --------------------------------------------------------------------------- */
+typedef struct {
+    int32_t B;            /* sequences                          1 <= B <= 65536     */
+    int32_t Hq;           /* query heads                                            */
+    int32_t Hkv;          /* KV heads, Hq % Hkv == 0, Hq / Hkv <= 128               */
+    int32_t d;            /* head width: 64 or 128                                  */
+    int32_t dtype;        /* reatt_dtype of every operand                           */
+    int32_t page;         /* tokens per page, a power of two                        */
+    int32_t max_pages;    /* page-table columns; max_pages * page <= 2^24           */
+    int32_t reserved;     /* 0                                                      */
+    int64_t N;            /* packed rows, 0 <= N < 2^28                             */
+    int64_t n_pages;      /* pages in each of the two pools, < 2^31                 */
+    int64_t q_stride;     /* elements between packed rows of q; 0 = Hq * d          */
+    int64_t k_stride;     /* ... of k; 0 = Hkv * d                                  */
+    int64_t v_stride;     /* ... of v; 0 = Hkv * d                                  */
+    int64_t q_rot_stride; /* ... of q_rot; 0 = Hq * d                               */
+    int64_t k_rot_stride; /* ... of k_rot; 0 = Hkv * d                              */
+    double rope_base;     /* RoPE base; 0 leaves q and k un-rotated                 */
+} reatt_paged_dims;
+
+/* Bytes of device workspace the paged calls with these dims may use (a
+ * multiple of 256, independent of N and of the lengths); the status word sits
+ * at its start, as in every workspace. */
+REATT_API int reatt_paged_workspace_bytes(const reatt_paged_dims *dims, size_t *bytes);
+
+/*
+ * Appends the packed new tokens to the paged caches.  Token i of sequence b
+ * has position p = past_len[b] + i; its k is rotated at p (as everywhere:
+ * pairs (i, i + d/2), frequency base^(-2i/d)) and stored, its v is stored
+ * as it is.  Beside reatt_append_kv, which appends un-rotated rows to the
+ * dense cache of reatt_step.
+ *   past_len  [B]: tokens cached before this call
+ *   q, q_rot  nullable together: q_rot receives q rotated at p (may be q)
+ *   k_rot     nullable: receives the rotated k as packed rows too (may be k)
+ *   seq_len   nullable, not past_len: receives past_len[b] + new tokens, the
+ *             lengths reatt_paged_decode then takes
+ */
+REATT_API int reatt_paged_append(const reatt_paged_dims *dims, const void *q, const void *k,
+                                 const void *v, const int32_t *cu_seqlens,
+                                 const int32_t *past_len, const int32_t *page_table, void *q_rot,
+                                 void *k_rot, void *k_pages, void *v_pages, int32_t *seq_len,
+                                 void *ws, reatt_stream stream);
+
+/*
+ * Attention of one new token per sequence over its pages:
+ *   out[b,j] = sum_{t < seq_len[b]} softmax_t(q[b,j] . K[b,t] / sqrt(d)) V[b,t]
+ * with head j on KV head j / (Hq / Hkv).  q: row b is sequence b's token,
+ * rotated already (N = B); its own key and value are in the cache, appended
+ * before.  out [B, Hq, d], dense.  seq_len[b] = 0 gives zeros.  fp32 softmax
+ * and accumulation; slots past seq_len are never used, whatever they hold.
+ */
+REATT_API int reatt_paged_decode(const reatt_paged_dims *dims, const void *q, const void *k_pages,
+                                 const void *v_pages, const int32_t *page_table,
+                                 const int32_t *seq_len, void *out, void *ws,
+                                 reatt_stream stream);
+
+/*
+ * Causal attention of whole prompts, packed:
+ *   out[i,j] = sum_{t <= i, same sequence} softmax_t(q[i,j] . k[t] / sqrt(d)) v[t]
+ * with head j on KV head j / (Hq / Hkv), q and k rotated already (the rotated
+ * copies of reatt_paged_append).  out [N, Hq, d], dense.  fp32 softmax and
+ * accumulation.  A token never reads a later token or another sequence,
+ * whatever those rows hold.  The page fields of dims are not used.
+ */
+REATT_API int reatt_prompt_attend(const reatt_paged_dims *dims, const void *q, const void *k,
+                                  const void *v, const int32_t *cu_seqlens, void *out, void *ws,
+                                  reatt_stream stream);
 
 /*
  * reatt_step without a caller-supplied workspace.  The pages have no

@@ -121,6 +121,7 @@ const char *reatt_status_string(int status)
     case REATT_EUNSUPPORTED: return "unsupported configuration (head width, dtype or size)";
     case REATT_ECUDA: return "CUDA error while launching";
     case REATT_ETIMEOUT: return "a kernel's bounded wait gave up";
+    case REATT_EPAGE: return "a cache page or length out of range was left out";
     default: return "unknown status";
     }
 }

@@ -138,4 +138,18 @@ cudaError_t launch_attend(const Geom &geo, const void *q, const float *kw, const
 // be written by the scan.
 int64_t decode_window_known(const Geom &geo);
 
+// Paged cache and packed prompts (paged.cuh holds the geometry).
+struct PagedGeom;
+cudaError_t launch_paged_append(const PagedGeom &g, const void *q, const void *k, const void *v,
+                                const int32_t *cu, const int32_t *past, const int32_t *table,
+                                void *q_rot, void *k_rot, void *k_pages, void *v_pages,
+                                int32_t *seq_len, void *ws, cudaStream_t st);
+// partials of the keys' split over CTAs
+size_t paged_decode_ws_bytes(const PagedGeom &g);
+cudaError_t launch_paged_decode(const PagedGeom &g, const void *q, const void *k_pages,
+                                const void *v_pages, const int32_t *table, const int32_t *lens,
+                                void *out, void *scratch, void *ws, cudaStream_t st);
+cudaError_t launch_prompt(const PagedGeom &g, const void *q, const void *k, const void *v,
+                          const int32_t *cu, void *out, void *ws, cudaStream_t st);
+
 }  // namespace reatt

@@ -1,0 +1,160 @@
+// What the decode kernels of the paged cache share: how the keys of a ragged
+// batch are dealt out to the CTAs, and the layout of their partial results.
+//
+// A unit is one sequence's keys under one KV head and one chunk of its query
+// heads; a tile is kTile keys of a unit.  All tiles of all units, in order, are
+// cut into as many equal ranges as there are CTAs, so a batch of any mix of
+// lengths loads every SM alike.  A unit that one range holds whole is finished
+// there; a range's first and last unit may be cut, and then leave (m, l, acc):
+// m the running maximum of the logits in the log2 domain, l the sum of
+// 2^(x - m), acc the sum of 2^(x - m) v.  Slot 2i of the partials is range i's
+// cut first unit (begun in an earlier range), slot 2i + 1 its cut last one
+// (begun here, continued later).
+#pragma once
+
+#include "paged.cuh"
+
+namespace reatt {
+
+constexpr int kPdWarps = 4;             // warps of a CTA; each takes its own keys of a tile
+constexpr int kPdThreads = kPdWarps * 32;
+constexpr int kPdStages = 3;            // tiles in flight per warp
+constexpr int kPdHalf = 4096;           // bytes of a warp's K (or V) rows of one tile
+constexpr int kPdStage = 2 * kPdHalf;
+
+// What range i left for the join (written by the main kernel, read by the join).
+struct PdMeta {
+    int32_t open_b, open_u;   // unit cut at the range's end that begins in it; open_b < 0: none
+    int32_t first;            // slot 2i: 0 unused, 1 ends its unit, 2 the unit goes on
+    int32_t pad;
+};
+
+struct PdArgs {
+    const void *q, *k_pages, *v_pages;
+    const int32_t *table, *lens;
+    void *out;
+    float *part_acc;   // [2 * ranges][HB][D]
+    float2 *part_ml;   // [2 * ranges][HB]
+    PdMeta *meta;      // [ranges]
+    void *ws;
+    int chunks;        // chunks of query heads per KV head
+    float scale;       // log2(e) / sqrt(d)
+};
+
+__device__ __forceinline__ int pd_len(const PagedGeom &geo, const int32_t *lens, int b)
+{
+    const int64_t n = lens[b], cap = geo.capacity();
+    return int(n < 0 ? 0 : (n > cap ? cap : n));
+}
+
+// Position in the list of tiles.
+struct PdWalk {
+    int b, u, tile, nt, len;
+    template <int TILE>
+    __device__ __forceinline__ void enter(const PagedGeom &geo, const int32_t *lens, int nb)
+    {
+        b = nb;
+        len = nt = 0;
+        while (b < geo.B) {
+            len = pd_len(geo, lens, b);
+            nt = (len + TILE - 1) / TILE;
+            if (nt > 0) break;
+            ++b;
+        }
+    }
+    template <int TILE>
+    __device__ __forceinline__ void next(const PagedGeom &geo, const int32_t *lens, int units)
+    {
+        if (++tile < nt) return;
+        tile = 0;
+        if (++u < units) return;
+        u = 0;
+        enter<TILE>(geo, lens, b + 1);
+    }
+};
+
+// This CTA's range of tiles: where it starts and how many tiles it holds.
+// Every thread of the CTA calls it.
+template <int TILE>
+__device__ __forceinline__ int64_t pd_range(const PagedGeom &geo, const int32_t *lens, int units,
+                                            PdWalk &w)
+{
+    __shared__ int64_t warp_sum[kPdWarps];
+    __shared__ int start[3];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (geo.B + kPdThreads - 1) / kPdThreads;
+    const int b0 = min(tid * per, geo.B), b1 = min(b0 + per, geo.B);
+    int64_t sum = 0;
+    for (int b = b0; b < b1; ++b) sum += int64_t((pd_len(geo, lens, b) + TILE - 1) / TILE) * units;
+    int64_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    if (tid == 0) start[0] = geo.B;
+    __syncthreads();
+    int64_t base = 0, total = 0;
+#pragma unroll
+    for (int x = 0; x < kPdWarps; ++x) {
+        if (x < warp) base += warp_sum[x];
+        total += warp_sum[x];
+    }
+    // with fewer tiles than CTAs the first `total` CTAs take one each
+    const int64_t ranges = min(total, int64_t(gridDim.x)), i = blockIdx.x;
+    const int64_t t0 = i < ranges ? total * i / ranges : total;
+    const int64_t t1 = i < ranges ? total * (i + 1) / ranges : total;
+    int64_t at = base + incl - sum;
+    if (t0 < t1 && t0 >= at && t0 < at + sum)
+        for (int b = b0; b < b1; ++b) {
+            const int nt = (pd_len(geo, lens, b) + TILE - 1) / TILE;
+            const int64_t n = int64_t(nt) * units;
+            if (t0 < at + n) {
+                start[0] = b;
+                start[1] = int((t0 - at) / nt);
+                start[2] = int((t0 - at) % nt);
+                break;
+            }
+            at += n;
+        }
+    __syncthreads();
+    w.b = start[0];
+    w.u = w.tile = w.nt = w.len = 0;
+    if (w.b < geo.B) {
+        w.u = start[1];
+        w.tile = start[2];
+        w.len = pd_len(geo, lens, w.b);
+        w.nt = (w.len + TILE - 1) / TILE;
+    }
+    return t1 - t0;
+}
+
+// 2^x on the special-function unit (relative error about 2^-22; 2^-inf = 0).
+__device__ __forceinline__ float pd_ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Weight of a partial with maximum m under the joint maximum M.
+__device__ __forceinline__ float pd_weight(float m, float M)
+{
+    return m == -INFINITY ? 0.f : pd_ex2(m - M);
+}
+
+// 16 bytes global -> shared without passing registers; fill = false writes zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool fill)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(fill ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+}  // namespace reatt

@@ -15,7 +15,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libreatt.so")
 
-OK, EINVAL, EUNSUPPORTED, ECUDA, ETIMEOUT = 0, 1, 2, 3, 4
+OK, EINVAL, EUNSUPPORTED, ECUDA, ETIMEOUT, EPAGE = 0, 1, 2, 3, 4, 5
 F32, BF16 = 0, 1
 
 EXPORTS = ["reatt_status_string", "reatt_num_spans", "reatt_window_max", "reatt_workspace_bytes",
@@ -23,7 +23,8 @@ EXPORTS = ["reatt_status_string", "reatt_num_spans", "reatt_window_max", "reatt_
            "reatt_attend", "reatt_step", "reatt_append_kv", "reatt_selftest_bounded_wait",
            "reatt_step_fixed_scratch", "reatt_fixed_scratch_address", "reatt_shard_plan", "reatt_shard_workspace_bytes",
            "reatt_shard_candidates", "reatt_shard_select", "reatt_shard_attend",
-           "reatt_merge_partials"]
+           "reatt_merge_partials", "reatt_paged_workspace_bytes", "reatt_paged_append",
+           "reatt_paged_decode", "reatt_prompt_attend"]
 
 
 class reatt_dims(ctypes.Structure):
@@ -38,6 +39,16 @@ class reatt_shard(ctypes.Structure):
     _fields_ = [("t_begin", ctypes.c_int64), ("t_end", ctypes.c_int64),
                 ("rows_cap", ctypes.c_int64), ("owns_current", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class reatt_paged_dims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("N", ctypes.c_int64), ("n_pages", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("q_rot_stride", ctypes.c_int64),
+                ("k_rot_stride", ctypes.c_int64), ("rope_base", ctypes.c_double)]
 
 
 class ReattError(RuntimeError):
@@ -74,6 +85,11 @@ lib.reatt_shard_candidates.argtypes = [_dp, _sp, _vp, _vp, _vp, _vp, _vp, _vp]
 lib.reatt_shard_select.argtypes = [_dp, ctypes.c_int32, _vp, _vp, _vp, _vp, _vp]
 lib.reatt_shard_attend.argtypes = [_dp, _sp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
 lib.reatt_merge_partials.argtypes = [_dp, ctypes.c_int32, _vp, _vp, _vp, _vp]
+_pp = ctypes.POINTER(reatt_paged_dims)
+lib.reatt_paged_workspace_bytes.argtypes = [_pp, ctypes.POINTER(ctypes.c_size_t)]
+lib.reatt_paged_append.argtypes = [_pp] + [_vp] * 13
+lib.reatt_paged_decode.argtypes = [_pp] + [_vp] * 8
+lib.reatt_prompt_attend.argtypes = [_pp] + [_vp] * 7
 for _name in EXPORTS[1:]:
     getattr(lib, _name).restype = ctypes.c_int
 
@@ -276,6 +292,83 @@ def reatt_merge_partials(dims, n_parts, part_ml_all, part_acc_all, out, stream=N
                                   _ptr(part_acc_all), _ptr(out), _stream(stream))
     if check:
         _check(rc, "reatt_merge_partials")
+    return rc
+
+
+# ----------------------------------------------------------------- paged cache, packed prompts
+def make_paged_dims(B, Hq, Hkv, d, dtype, N, page=1, max_pages=1, n_pages=1, rope_base=0.0,
+                    q_stride=0, k_stride=0, v_stride=0, q_rot_stride=0,
+                    k_rot_stride=0) -> reatt_paged_dims:
+    """Dims of the paged calls (strides in elements between packed rows, 0 = dense)."""
+    if isinstance(dtype, str):
+        dtype = F32 if dtype == "f32" else BF16
+    elif isinstance(dtype, torch.dtype):
+        dtype = F32 if dtype == torch.float32 else BF16
+    return reatt_paged_dims(int(B), int(Hq), int(Hkv), int(d), int(dtype), int(page),
+                            int(max_pages), 0, int(N), int(n_pages), int(q_stride), int(k_stride),
+                            int(v_stride), int(q_rot_stride), int(k_rot_stride), float(rope_base))
+
+
+def _paged_ptrs(where, code, data, ints, ws):
+    """Device addresses of a paged call's tensors.  What the library cannot see
+    is checked here: every tensor lives on the current device and has the dtype
+    of the dims (int32 for lengths and tables).  Addresses (int) and None pass."""
+    want = torch.bfloat16 if code == BF16 else torch.float32
+    out, dev = [], None
+    for group, dt in ((data, want), (ints, torch.int32), ((ws,), None)):
+        for t in group:
+            if t is None or isinstance(t, int):
+                out.append(t)
+                continue
+            if dev is None and t.is_cuda:
+                dev = torch.cuda.current_device()
+            if t.get_device() != dev or (dt is not None and t.dtype is not dt):
+                raise ReattError(EINVAL, f"{where}: a tensor of {t.dtype} on {t.device}, wanted "
+                                         f"{dt or 'any dtype'} on the current CUDA device")
+            out.append(t.data_ptr())
+    return out
+
+
+def reatt_paged_workspace_bytes(dims) -> int:
+    v = ctypes.c_size_t()
+    _check(lib.reatt_paged_workspace_bytes(ctypes.byref(dims), ctypes.byref(v)),
+           "reatt_paged_workspace_bytes")
+    return v.value
+
+
+def reatt_paged_append(dims, q, k, v, cu_seqlens, past_len, page_table, q_rot, k_rot, k_pages,
+                       v_pages, seq_len, ws, stream=None, check=True):
+    """Append packed new tokens to the paged caches, k (and q) rotated at their
+    positions; q/q_rot, k_rot and seq_len may be None."""
+    (pq, pk, pv, pqr, pkr, pkp, pvp, pcu, ppast, ptab, plen, pws) = _paged_ptrs(
+        "reatt_paged_append", dims.dtype, (q, k, v, q_rot, k_rot, k_pages, v_pages),
+        (cu_seqlens, past_len, page_table, seq_len), ws)
+    rc = lib.reatt_paged_append(ctypes.byref(dims), pq, pk, pv, pcu, ppast, ptab, pqr, pkr, pkp,
+                                pvp, plen, pws, _stream(stream))
+    if check:
+        _check(rc, "reatt_paged_append")
+    return rc
+
+
+def reatt_paged_decode(dims, q, k_pages, v_pages, page_table, seq_len, out, ws, stream=None,
+                       check=True):
+    """Attention of one new token per sequence over its pages."""
+    pq, pkp, pvp, pout, ptab, plen, pws = _paged_ptrs(
+        "reatt_paged_decode", dims.dtype, (q, k_pages, v_pages, out), (page_table, seq_len), ws)
+    rc = lib.reatt_paged_decode(ctypes.byref(dims), pq, pkp, pvp, ptab, plen, pout, pws,
+                                _stream(stream))
+    if check:
+        _check(rc, "reatt_paged_decode")
+    return rc
+
+
+def reatt_prompt_attend(dims, q, k, v, cu_seqlens, out, ws, stream=None, check=True):
+    """Causal attention of whole prompts, packed."""
+    pq, pk, pv, pout, pcu, pws = _paged_ptrs("reatt_prompt_attend", dims.dtype, (q, k, v, out),
+                                             (cu_seqlens,), ws)
+    rc = lib.reatt_prompt_attend(ctypes.byref(dims), pq, pk, pv, pcu, pout, pws, _stream(stream))
+    if check:
+        _check(rc, "reatt_prompt_attend")
     return rc
 
 

@@ -149,6 +149,9 @@ size_t paged_decode_ws_bytes(const PagedGeom &g);
 cudaError_t launch_paged_decode(const PagedGeom &g, const void *q, const void *k_pages,
                                 const void *v_pages, const int32_t *table, const int32_t *lens,
                                 void *out, void *scratch, void *ws, cudaStream_t st);
+// bf16, on the tensor cores
+cudaError_t launch_prompt_tc(const PagedGeom &g, const void *q, const void *k, const void *v,
+                             const int32_t *cu, void *out, void *ws, cudaStream_t st);
 cudaError_t launch_prompt(const PagedGeom &g, const void *q, const void *k, const void *v,
                           const int32_t *cu, void *out, void *ws, cudaStream_t st);
 

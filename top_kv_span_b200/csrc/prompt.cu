@@ -1,4 +1,4 @@
-// Causal attention of packed prompts on the CUDA cores.
+// Causal attention of packed prompts on the CUDA cores (fp32).
 //
 //   o_i = sum_{t <= i} softmax_t(q_i.k_t / sqrt(d)) v_t   within each sequence
 //
@@ -6,7 +6,6 @@
 // a time with the running maximum and sum of the softmax.  Scores and output
 // stay in registers (4 x 4 and 4 x d/16 per thread); the arithmetic is fp32
 // fused multiply-adds, which bound it.
-#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -18,18 +17,6 @@ namespace {
 
 constexpr int kPrThreads = 256;
 constexpr int kPrTile = 64;   // query tokens of a CTA, and keys of a tile
-
-template <typename T> __device__ __forceinline__ void store4(T *p, const float (&v)[4]);
-template <> __device__ __forceinline__ void store4<float>(float *p, const float (&v)[4])
-{
-    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-}
-template <> __device__ __forceinline__ void store4<uint16_t>(uint16_t *p, const float (&v)[4])
-{
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-    *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&a),
-                                               *reinterpret_cast<const uint32_t *>(&b));
-}
 
 template <int D> struct PrSmem {
     static constexpr int QS = D + 4, PS = kPrTile + 4;   // padded rows: conflict-free columns
@@ -169,8 +156,8 @@ prompt_kernel(PagedGeom geo, const T *__restrict__ q, const T *__restrict__ k,
             T *dst = out + (int64_t(blk.begin + blk.q0 + ty * 4 + r) * geo.Hq + j) * D;
 #pragma unroll
             for (int c = 0; c < OC; c += 4) {
-                const float w[4] = {o[r][c] * il, o[r][c + 1] * il, o[r][c + 2] * il, o[r][c + 3] * il};
-                store4(dst + (c / 4) * 64 + tx * 4, w);
+                *reinterpret_cast<float4 *>(dst + (c / 4) * 64 + tx * 4) =
+                    make_float4(o[r][c] * il, o[r][c + 1] * il, o[r][c + 2] * il, o[r][c + 3] * il);
             }
         }
     }
@@ -198,10 +185,8 @@ cudaError_t run(const PagedGeom &g, const void *q, const void *k, const void *v,
 cudaError_t launch_prompt(const PagedGeom &g, const void *q, const void *k, const void *v,
                           const int32_t *cu, void *out, void *ws, cudaStream_t st)
 {
-    (void)ws;
     if (g.N == 0) return cudaSuccess;
-    if (g.dtype == REATT_BF16)
-        return g.d == 128 ? run<uint16_t, 128>(g, q, k, v, cu, out, st) : run<uint16_t, 64>(g, q, k, v, cu, out, st);
+    if (g.dtype == REATT_BF16) return launch_prompt_tc(g, q, k, v, cu, out, ws, st);
     return g.d == 128 ? run<float, 128>(g, q, k, v, cu, out, st) : run<float, 64>(g, q, k, v, cu, out, st);
 }
 

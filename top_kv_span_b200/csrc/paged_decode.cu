@@ -41,16 +41,6 @@ template <> __device__ __forceinline__ void load_slice<4>(const float *p, float 
     const float4 t = *reinterpret_cast<const float4 *>(p);
     v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
 }
-template <int E> __device__ __forceinline__ void load_slice(const uint16_t *p, float (&v)[E])
-{
-#pragma unroll
-    for (int e = 0; e < E; e += 2) {
-        const uint32_t t = *reinterpret_cast<const uint32_t *>(p + e);
-        v[e] = bf16lo(t);
-        v[e + 1] = bf16hi(t);
-    }
-}
-
 // Elements [offset, ...) of the page row of key `key`, or < 0.
 __device__ __forceinline__ int64_t key_row(const PagedGeom &geo, int id, int h, int key, int D)
 {
@@ -59,87 +49,157 @@ __device__ __forceinline__ int64_t key_row(const PagedGeom &geo, int id, int h, 
              (key & ((1 << geo.page_shift) - 1)))) * D;
 }
 
-// HB query heads of one KV head per unit.  A lane owns D/32 elements of every
+// One warp's stream of its K and V rows of the tiles, `n` tiles from `at` on, through
+// its ring in shared memory.  The page of the next tile's rows is looked up one
+// tile ahead, so that its latency is not waited for.
+template <typename T, int D, bool SWIZZLE> struct PdStream {
+    static constexpr int RB = D * int(sizeof(T));   // bytes of a row
+    static constexpr int KT = kPdHalf / RB;         // keys of a warp's part of a tile
+    static constexpr int TILE = KT * kPdWarps;
+    static constexpr int LPR = RB / 16;             // 16-byte words of a row
+    static_assert(KT <= 32, "a lane looks up one key");
+
+    const PagedGeom &geo;
+    const PdArgs &a;
+    PdWalk at;
+    int64_t n, loaded = 0;
+    int units, key_of_lane, id;
+    uint32_t ring;
+
+    __device__ __forceinline__ PdStream(const PagedGeom &g, const PdArgs &args, const PdWalk &w,
+                                        int64_t tiles, int u, uint32_t ring_addr)
+        : geo(g), a(args), at(w), n(tiles), units(u), ring(ring_addr)
+    {
+        key_of_lane = int(threadIdx.x >> 5) * KT + int(threadIdx.x & 31);
+        look_up();
+    }
+    __device__ __forceinline__ bool mine(int key) const
+    {
+        return int(threadIdx.x & 31) < KT && key < at.len;
+    }
+    __device__ __forceinline__ void look_up()
+    {
+        const int key = at.tile * TILE + key_of_lane;
+        id = mine(key) ? a.table[int64_t(at.b) * geo.max_pages + (key >> geo.page_shift)] : 0;
+    }
+    // Issue the next tile's copies (none past the end); one group either way.
+    __device__ __forceinline__ void load()
+    {
+        if (loaded < n) {
+            const int lane = threadIdx.x & 31, key = at.tile * TILE + key_of_lane;
+            int64_t off = -1;
+            if (mine(key)) {
+                off = key_row(geo, id, at.u / a.chunks, key, D);
+                if (off < 0) report_status(a.ws, REATT_EPAGE);
+            }
+            const uint32_t st = ring + uint32_t(loaded % kPdStages) * kPdStage;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = i * (32 / LPR) + lane / LPR, c = lane % LPR;
+                const int64_t o = __shfl_sync(0xffffffffu, off, r);
+                const uint32_t dst = st + uint32_t(r * RB + (SWIZZLE ? c ^ (r & 7) : c) * 16);
+                const int64_t src = (o < 0 ? 0 : o) * int64_t(sizeof(T)) + c * 16;
+                cp_async16(dst, static_cast<const uint8_t *>(a.k_pages) + src, o >= 0);
+                cp_async16(dst + kPdHalf, static_cast<const uint8_t *>(a.v_pages) + src, o >= 0);
+            }
+            if (++loaded < n) {
+                at.next<TILE>(geo, a.lens, units);
+                look_up();
+            }
+        }
+        cp_async_commit();
+    }
+};
+
+// What a range does besides its tiles: zeros for sequences without a key, and the
+// status of lengths out of range.
+template <typename T, int D>
+__device__ __forceinline__ void pd_empty(const PagedGeom &geo, const PdArgs &a)
+{
+    for (int b = blockIdx.x; b < geo.B; b += gridDim.x) {
+        const int len = pd_len(geo, a.lens, b);
+        if (len == 0)
+            for (int i = threadIdx.x; i < geo.Hq * D; i += kPdThreads)
+                store_elem(static_cast<T *>(a.out) + int64_t(b) * geo.Hq * D + i, 0.f);
+        if (threadIdx.x == 0 && len != a.lens[b]) report_status(a.ws, REATT_EPAGE);
+    }
+}
+
+// Joins the warps' (m, l, o) of a unit's part, which they have left in red_ml and
+// red_o, and finishes the unit or leaves the part for the join kernel.  Every thread
+// of the CTA calls it after a barrier, and passes another one after it.
+template <typename T, int D, int HB>
+__device__ __forceinline__ void pd_finish(const PagedGeom &geo, const PdArgs &a, const PdWalk &w,
+                                          bool begins, bool ends, const float2 (*red_ml)[HB],
+                                          const float *red_o)
+{
+    const int h = w.u / a.chunks, j0 = (w.u % a.chunks) * HB, nh = min(HB, geo.g - j0);
+    const bool whole = begins && ends;
+    const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
+    for (int y = threadIdx.x; y < nh * D; y += kPdThreads) {
+        const int j = y / D, c = y - j * D;
+        float M = red_ml[0][j].x;
+#pragma unroll
+        for (int i = 1; i < kPdWarps; ++i) M = fmaxf(M, red_ml[i][j].x);
+        float L = 0.f, acc = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPdWarps; ++i) {
+            const float f = pd_weight(red_ml[i][j].x, M);
+            L += f * red_ml[i][j].y;
+            acc += f * red_o[(i * HB + j) * D + c];
+        }
+        if (whole) {
+            store_elem(static_cast<T *>(a.out) + (int64_t(w.b) * geo.Hq + h * geo.g + j0 + j) * D + c,
+                       acc / L);
+        } else {
+            a.part_acc[(int64_t(slot) * HB + j) * D + c] = acc;
+            if (c == 0) a.part_ml[slot * HB + j] = make_float2(M, L);
+        }
+    }
+    if (threadIdx.x == 0 && !whole) {
+        if (begins) {
+            a.meta[blockIdx.x].open_b = w.b;
+            a.meta[blockIdx.x].open_u = w.u;
+        } else {
+            a.meta[blockIdx.x].first = ends ? 1 : 2;
+        }
+    }
+}
+
+// fp32: HB query heads of one KV head per unit.  A lane owns D/32 elements of every
 // row; the dot products of a tile's keys and heads are summed over the lanes by
 // a transposed butterfly (31 shuffles for 32 sums), which leaves one (key, head)
 // pair per lane for the exponentials.
-template <typename T, int D, int HB>
+template <int D, int HB>
 __global__ void __launch_bounds__(kPdThreads)
-paged_decode_kernel(PagedGeom geo, PdArgs a)
+paged_decode_f32_kernel(PagedGeom geo, PdArgs a)
 {
-    constexpr int RB = D * int(sizeof(T));   // bytes of a row
-    constexpr int KT = kPdHalf / RB;         // keys of a warp's part of a tile
-    constexpr int TILE = KT * kPdWarps;
+    using Stream = PdStream<float, D, false>;
+    constexpr int KT = Stream::KT, TILE = Stream::TILE;
     constexpr int E = D / 32;                // elements of a row per lane
-    constexpr int LPR = RB / 16;             // 16-byte words of a row
     constexpr int NB = KT * HB / 32;         // butterflies per tile part
-    static_assert(NB * 32 == KT * HB && KT <= 32, "tile shape");
+    static_assert(NB * 32 == KT * HB, "tile shape");
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float red_ml[kPdWarps][HB][2];
+    __shared__ float2 red_ml[kPdWarps][HB];
     float *red_o = reinterpret_cast<float *>(smem + kPdWarps * kPdStages * kPdStage);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int units = geo.Hkv * a.chunks;
     pdl_trigger();   // the join may be scheduled; it waits for this grid's end
     pdl_wait();
-
-    // sequences without a key: zeros
-    for (int b = blockIdx.x; b < geo.B; b += gridDim.x) {
-        const int len = pd_len(geo, a.lens, b);
-        if (len == 0)
-            for (int i = tid; i < geo.Hq * D; i += kPdThreads)
-                store_elem(static_cast<T *>(a.out) + int64_t(b) * geo.Hq * D + i, 0.f);
-        if (tid == 0 && len != a.lens[b]) report_status(a.ws, REATT_EPAGE);
-    }
-
+    pd_empty<float, D>(geo, a);
     PdWalk cw;
     const int64_t n = pd_range<TILE>(geo, a.lens, units, cw);
     if (tid == 0) a.meta[blockIdx.x] = PdMeta{-1, 0, 0, 0};
     if (n == 0) return;
-    PdWalk lw = cw;
-    uint8_t *ring = smem + warp * kPdStages * kPdStage;
-    const uint32_t ring_addr = smem_addr(ring);
-
-    auto table_of = [&](const PdWalk &w) {
-        const int key = w.tile * TILE + warp * KT + lane;
-        return lane < KT && key < w.len
-                   ? a.table[int64_t(w.b) * geo.max_pages + (key >> geo.page_shift)]
-                   : 0;
-    };
-    int id = table_of(lw);   // this lane's page of the tile to load next
-    int64_t loaded = 0;
-    auto load = [&]() {
-        if (loaded < n) {
-            const int key0 = lw.tile * TILE + warp * KT, h = lw.u / a.chunks;
-            int64_t off = -1;
-            if (lane < KT && key0 + lane < lw.len) {
-                off = key_row(geo, id, h, key0 + lane, D);
-                if (off < 0) report_status(a.ws, REATT_EPAGE);
-            }
-            const uint32_t st = ring_addr + uint32_t(loaded % kPdStages) * kPdStage;
+    const uint8_t *ring = smem + warp * kPdStages * kPdStage;
+    Stream stream(geo, a, cw, n, units, smem_addr(ring));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = i * (32 / LPR) + lane / LPR;
-                const int64_t o = __shfl_sync(0xffffffffu, off, r);
-                const uint32_t dst = st + uint32_t(i * 512 + lane * 16);
-                const int64_t src = (o < 0 ? 0 : o) * int64_t(sizeof(T)) + (lane % LPR) * 16;
-                cp_async16(dst, static_cast<const uint8_t *>(a.k_pages) + src, o >= 0);
-                cp_async16(dst + kPdHalf, static_cast<const uint8_t *>(a.v_pages) + src, o >= 0);
-            }
-            if (++loaded < n) {
-                lw.next<TILE>(geo, a.lens, units);
-                id = table_of(lw);
-            }
-        }
-        cp_async_commit();
-    };
-#pragma unroll
-    for (int s = 0; s < kPdStages - 1; ++s) load();
+    for (int s = 0; s < kPdStages - 1; ++s) stream.load();
 
     float qv[HB][E], o[HB][E], m = -INFINITY, l = 0.f;   // m, l: of head lane % HB
     bool fresh = true;
-    const int64_t seg0 = cw.tile;   // first tile of the current segment
-    int64_t seg_begin = seg0;
+    bool begins = cw.tile == 0;   // this part of the unit starts at its first key
     for (int64_t i = 0; i < n; ++i) {
         const int h = cw.u / a.chunks, j0 = (cw.u % a.chunks) * HB;   // first query head of the unit
         const int nh = min(HB, geo.g - j0);
@@ -149,7 +209,7 @@ paged_decode_kernel(PagedGeom geo, PdArgs a)
 #pragma unroll
                 for (int e = 0; e < E; ++e) qv[j][e] = o[j][e] = 0.f;
                 if (j < nh)
-                    load_slice<E>(static_cast<const T *>(a.q) + int64_t(cw.b) * geo.qs +
+                    load_slice<E>(static_cast<const float *>(a.q) + int64_t(cw.b) * geo.qs +
                                       int64_t(h * geo.g + j0 + j) * D + lane * E,
                                   qv[j]);
             }
@@ -157,11 +217,11 @@ paged_decode_kernel(PagedGeom geo, PdArgs a)
             l = 0.f;
             fresh = false;
         }
-        load();
+        stream.load();
         cp_async_wait<kPdStages - 1>();
         __syncwarp();
-        const T *kt = reinterpret_cast<const T *>(ring + (i % kPdStages) * kPdStage);
-        const T *vt = reinterpret_cast<const T *>(ring + (i % kPdStages) * kPdStage + kPdHalf);
+        const float *kt = reinterpret_cast<const float *>(ring + (i % kPdStages) * kPdStage);
+        const float *vt = kt + kPdHalf / 4;
         const int key0 = cw.tile * TILE + warp * KT;
         float x[NB];
 #pragma unroll
@@ -228,50 +288,213 @@ paged_decode_kernel(PagedGeom geo, PdArgs a)
             // join the warps, then finish the unit or leave it for the join kernel
 #pragma unroll
             for (int w = HB; w < 32; w <<= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
-            if (lane < HB) {
-                red_ml[warp][lane][0] = m;
-                red_ml[warp][lane][1] = l;
-            }
+            if (lane < HB) red_ml[warp][lane] = make_float2(m, l);
 #pragma unroll
             for (int j = 0; j < HB; ++j)
 #pragma unroll
                 for (int e = 0; e < E; ++e) red_o[(warp * HB + j) * D + lane * E + e] = o[j][e];
             __syncthreads();
-            const bool begins = seg_begin == 0, whole = begins && unit_end;
-            const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
-            for (int y = tid; y < HB * D; y += kPdThreads) {
-                const int j = y / D, c = y - j * D;
-                float M = red_ml[0][j][0];
-#pragma unroll
-                for (int w = 1; w < kPdWarps; ++w) M = fmaxf(M, red_ml[w][j][0]);
-                float L = 0.f, acc = 0.f;
-#pragma unroll
-                for (int w = 0; w < kPdWarps; ++w) {
-                    const float f = pd_weight(red_ml[w][j][0], M);
-                    L += f * red_ml[w][j][1];
-                    acc += f * red_o[(w * HB + j) * D + c];
-                }
-                if (whole) {
-                    if (j < nh)
-                        store_elem(static_cast<T *>(a.out) +
-                                       (int64_t(cw.b) * geo.Hq + h * geo.g + j0 + j) * D + c,
-                                   acc / L);
-                } else {
-                    a.part_acc[(int64_t(slot) * HB + j) * D + c] = acc;
-                    if (c == 0) a.part_ml[slot * HB + j] = make_float2(M, L);
-                }
-            }
-            if (tid == 0 && !whole) {
-                if (begins) {
-                    a.meta[blockIdx.x].open_b = cw.b;
-                    a.meta[blockIdx.x].open_u = cw.u;
-                } else {
-                    a.meta[blockIdx.x].first = unit_end ? 1 : 2;
-                }
-            }
+            pd_finish<float, D, HB>(geo, a, cw, begins, unit_end, red_ml, red_o);
             __syncthreads();
-            fresh = true;
-            seg_begin = 0;
+            fresh = begins = true;
+        }
+        if (i + 1 < n) cw.next<TILE>(geo, a.lens, units);
+    }
+    cp_async_wait<0>();
+}
+
+// D (16 x 8, fp32) += A (16 x 16, bf16) . B (16 x 8, bf16)
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <bool TRANS> __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr)
+{
+    if constexpr (TRANS)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// Transposes an 8 x 8 bf16 matrix that the warp holds two elements a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// bf16: the products run on the tensor cores with the keys as the rows, so that up
+// to 8 query heads of the KV head are the 8 columns of one product (HT such
+// groups): S^T = K.Q^T, 16 keys x 8 heads, and O^T += V^T.P^T, 16 elements of d x 8
+// heads.  K and V come by ldmatrix from rows whose 16-byte words are swizzled by
+// the row's low three bits (no bank conflicts), S^T turns into the operand P^T by
+// 8 x 8 transposes between registers, P rounds to bf16 there (the row sum takes the
+// unrounded value).  The reference maximum of a head moves only when some logit
+// exceeds it by 2^8, so most tiles need no reduction over the keys.
+// Memory bounds it: per 16 keys a warp issues about 250 instructions, a fifth of what
+// an SM's share of the bandwidth leaves time for.
+constexpr float kPdMove = 8.f;
+template <int D, int HT>
+__global__ void __launch_bounds__(kPdThreads)
+paged_decode_bf16_kernel(PagedGeom geo, PdArgs a)
+{
+    using Stream = PdStream<uint16_t, D, true>;
+    constexpr int KT = Stream::KT, TILE = Stream::TILE, RB = Stream::RB, HB = 8 * HT;
+    constexpr int KG = KT / 16;   // groups of 16 keys
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float2 red_ml[kPdWarps][HB];
+    float *red_o = reinterpret_cast<float *>(smem + kPdWarps * kPdStages * kPdStage);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int gr = lane >> 2, tc = lane & 3;   // row and column pair of this lane in a product
+    const int units = geo.Hkv * a.chunks;
+    pdl_trigger();   // the join may be scheduled; it waits for this grid's end
+    pdl_wait();
+    pd_empty<uint16_t, D>(geo, a);
+    PdWalk cw;
+    const int64_t n = pd_range<TILE>(geo, a.lens, units, cw);
+    if (tid == 0) a.meta[blockIdx.x] = PdMeta{-1, 0, 0, 0};
+    if (n == 0) return;
+    const uint32_t ring = smem_addr(smem + warp * kPdStages * kPdStage);
+    Stream stream(geo, a, cw, n, units, ring);
+#pragma unroll
+    for (int s = 0; s < kPdStages - 1; ++s) stream.load();
+
+    // this lane's rows for ldmatrix, and the swizzle of its words
+    const uint32_t k_row = uint32_t((lane & 15) * RB), v_row = uint32_t(((lane & 7) + (lane >> 4) * 8) * RB);
+    const uint32_t k_word = lane >> 4, v_word = (lane >> 3) & 1, swz = lane & 7;
+
+    uint32_t q[HT][D / 16][2];
+    float o[HT][D / 16][4], m[HT][2], l[HT][2];   // of heads 8 ht + 2 tc, + 1
+    bool fresh = true;
+    bool begins = cw.tile == 0;   // this part of the unit starts at its first key
+    for (int64_t i = 0; i < n; ++i) {
+        if (fresh) {
+            const int h = cw.u / a.chunks, j0 = (cw.u % a.chunks) * HB, nh = min(HB, geo.g - j0);
+#pragma unroll
+            for (int t = 0; t < HT; ++t) {
+                const bool in = 8 * t + gr < nh;
+                const uint32_t *src = reinterpret_cast<const uint32_t *>(
+                    static_cast<const uint16_t *>(a.q) + int64_t(cw.b) * geo.qs +
+                    int64_t(h * geo.g + j0 + (in ? 8 * t + gr : 0)) * D);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    q[t][ks][0] = in ? src[ks * 8 + tc] : 0u;
+                    q[t][ks][1] = in ? src[ks * 8 + 4 + tc] : 0u;
+                }
+#pragma unroll
+                for (int dt = 0; dt < D / 16; ++dt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[t][dt][e] = 0.f;
+                m[t][0] = m[t][1] = -INFINITY;
+                l[t][0] = l[t][1] = 0.f;
+            }
+            fresh = false;
+        }
+        stream.load();
+        cp_async_wait<kPdStages - 1>();
+        __syncwarp();
+        const uint32_t kt = ring + uint32_t(i % kPdStages) * kPdStage, vt = kt + kPdHalf;
+        const int key0 = cw.tile * TILE + warp * KT;
+        float x[KG][HT][4];
+#pragma unroll
+        for (int kg = 0; kg < KG; ++kg) {
+#pragma unroll
+            for (int t = 0; t < HT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[kg][t][e] = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                uint32_t f[4];
+                ldmatrix4<false>(f, kt + uint32_t(kg * 16 * RB) + k_row + (((2 * ks + k_word) ^ swz) << 4));
+#pragma unroll
+                for (int t = 0; t < HT; ++t) mma16816(x[kg][t], f, q[t][ks][0], q[t][ks][1]);
+            }
+        }
+        bool lift = false;
+#pragma unroll
+        for (int kg = 0; kg < KG; ++kg)
+#pragma unroll
+            for (int t = 0; t < HT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int key = key0 + kg * 16 + gr + (e >> 1) * 8;
+                    x[kg][t][e] = key < cw.len ? x[kg][t][e] * a.scale : -INFINITY;
+                    lift |= x[kg][t][e] > m[t][e & 1] + kPdMove;
+                }
+        if (__any_sync(0xffffffffu, lift)) {
+#pragma unroll
+            for (int t = 0; t < HT; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mx = fmaxf(x[0][t][e], x[0][t][e + 2]);
+#pragma unroll
+                    for (int kg = 1; kg < KG; ++kg) mx = fmaxf(mx, fmaxf(x[kg][t][e], x[kg][t][e + 2]));
+#pragma unroll
+                    for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+                    const float mn = fmaxf(m[t][e], mx), f = pd_weight(m[t][e], mn);
+                    m[t][e] = mn;
+                    l[t][e] *= f;
+#pragma unroll
+                    for (int dt = 0; dt < D / 16; ++dt) {
+                        o[t][dt][e] *= f;
+                        o[t][dt][e + 2] *= f;
+                    }
+                }
+        }
+#pragma unroll
+        for (int kg = 0; kg < KG; ++kg) {
+            uint32_t p[HT][2];
+#pragma unroll
+            for (int t = 0; t < HT; ++t) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    // a masked key is -inf (also before any maximum is known): no weight
+                    const float w = x[kg][t][e] == -INFINITY ? 0.f : pd_ex2(x[kg][t][e] - m[t][e & 1]);
+                    l[t][e & 1] += w;
+                    x[kg][t][e] = w;
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const __nv_bfloat162 b2 = __floats2bfloat162_rn(x[kg][t][2 * e], x[kg][t][2 * e + 1]);
+                    p[t][e] = transpose8(*reinterpret_cast<const uint32_t *>(&b2));
+                }
+            }
+#pragma unroll
+            for (int dt = 0; dt < D / 16; ++dt) {
+                uint32_t f[4];
+                ldmatrix4<true>(f, vt + uint32_t(kg * 16 * RB) + v_row + (((2 * dt + v_word) ^ swz) << 4));
+#pragma unroll
+                for (int t = 0; t < HT; ++t) mma16816(o[t][dt], f, p[t][0], p[t][1]);
+            }
+        }
+        __syncwarp();   // the stage may be refilled
+        const bool unit_end = cw.tile + 1 == cw.nt;
+        if (unit_end || i + 1 == n) {
+            // join the warps, then finish the unit or leave it for the join kernel
+#pragma unroll
+            for (int t = 0; t < HT; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int w = 4; w < 32; w <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], w);
+                    const int j = 8 * t + 2 * tc + e;
+                    if (gr == 0) red_ml[warp][j] = make_float2(m[t][e], l[t][e]);
+#pragma unroll
+                    for (int dt = 0; dt < D / 16; ++dt) {
+                        red_o[(warp * HB + j) * D + dt * 16 + gr] = o[t][dt][e];
+                        red_o[(warp * HB + j) * D + dt * 16 + gr + 8] = o[t][dt][e + 2];
+                    }
+                }
+            __syncthreads();
+            pd_finish<uint16_t, D, HB>(geo, a, cw, begins, unit_end, red_ml, red_o);
+            __syncthreads();
+            fresh = begins = true;
         }
         if (i + 1 < n) cw.next<TILE>(geo, a.lens, units);
     }
@@ -320,25 +543,36 @@ paged_decode_join_kernel(PagedGeom geo, PdArgs a)
 constexpr int kMaxHeads = 16;   // query heads of a unit, at most
 
 template <typename T, int D, int HB>
-cudaError_t run(const PagedGeom &g, PdArgs a, int ranges, cudaStream_t st)
+cudaError_t run(void (*kern)(PagedGeom, PdArgs), const PagedGeom &g, PdArgs a, cudaStream_t st)
 {
     a.chunks = (g.g + HB - 1) / HB;
-    auto kern = paged_decode_kernel<T, D, HB>;
     const size_t smem = size_t(kPdWarps) * kPdStages * kPdStage + size_t(kPdWarps) * HB * D * 4;
+    // one range per CTA that the SMs hold at once
+    const int ranges = num_sms() * (2 * (smem + 2048) <= 228 * 1024 ? 2 : 1);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, dim3(unsigned(ranges)), dim3(kPdThreads), smem, st, g, a);
     if (e != cudaSuccess) return e;
     return launch_pdl(paged_decode_join_kernel<T, D, HB>, dim3(unsigned(ranges)), dim3(256), 0, st, g, a);
 }
+// Query heads of a unit: as few as hold the group, at most 8 (fp32, whose products
+// cost an instruction each) or 16.
+template <int D> cudaError_t run_d(const PagedGeom &g, const PdArgs &a, cudaStream_t st)
+{
+    if (g.dtype == REATT_BF16)
+        return g.g <= 8 ? run<uint16_t, D, 8>(paged_decode_bf16_kernel<D, 1>, g, a, st)
+                        : run<uint16_t, D, 16>(paged_decode_bf16_kernel<D, 2>, g, a, st);
+    return g.g <= 4 ? run<float, D, 4>(paged_decode_f32_kernel<D, 4>, g, a, st)
+                    : run<float, D, 8>(paged_decode_f32_kernel<D, 8>, g, a, st);
+}
 
-int ranges_of() { return 2 * num_sms(); }   // two CTAs fit an SM
+int max_ranges() { return 2 * num_sms(); }
 
 }  // namespace
 
 size_t paged_decode_ws_bytes(const PagedGeom &g)
 {
-    const size_t n = size_t(ranges_of());
+    const size_t n = size_t(max_ranges());
     return n * sizeof(PdMeta) + 2 * n * kMaxHeads * (sizeof(float2) + size_t(g.d) * sizeof(float));
 }
 
@@ -346,19 +580,14 @@ cudaError_t launch_paged_decode(const PagedGeom &g, const void *q, const void *k
                                 const void *v_pages, const int32_t *table, const int32_t *lens,
                                 void *out, void *scratch, void *ws, cudaStream_t st)
 {
-    const int n = ranges_of();
+    const int n = max_ranges();
     uint8_t *p = static_cast<uint8_t *>(scratch);
     PdArgs a{q, k_pages, v_pages, table, lens, out, nullptr, nullptr, nullptr, ws, 1,
              float(1.4426950408889634 / sqrt(double(g.d)))};
     a.part_acc = reinterpret_cast<float *>(p);
     a.part_ml = reinterpret_cast<float2 *>(p + size_t(2 * n) * kMaxHeads * g.d * sizeof(float));
     a.meta = reinterpret_cast<PdMeta *>(a.part_ml + size_t(2 * n) * kMaxHeads);
-    if (g.dtype == REATT_BF16) {
-        if (g.d == 128) return g.g <= 4 ? run<uint16_t, 128, 4>(g, a, n, st) : run<uint16_t, 128, 8>(g, a, n, st);
-        return g.g <= 4 ? run<uint16_t, 64, 4>(g, a, n, st) : run<uint16_t, 64, 8>(g, a, n, st);
-    }
-    if (g.d == 128) return g.g <= 4 ? run<float, 128, 4>(g, a, n, st) : run<float, 128, 8>(g, a, n, st);
-    return g.g <= 4 ? run<float, 64, 4>(g, a, n, st) : run<float, 64, 8>(g, a, n, st);
+    return g.d == 128 ? run_d<128>(g, a, st) : run_d<64>(g, a, st);
 }
 
 }  // namespace reatt

@@ -13,6 +13,8 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
+#include <algorithm>
+
 #include "kernels.h"
 #include "paged_decode.cuh"
 
@@ -62,15 +64,23 @@ template <typename T, int D, bool SWIZZLE> struct PdStream {
     const PagedGeom &geo;
     const PdArgs &a;
     PdWalk at;
-    int64_t n, loaded = 0;
-    int units, key_of_lane, id;
-    uint32_t ring;
+    int64_t left;              // tiles not issued yet
+    int units, slot = 0, key_of_lane, id;
+    uint32_t ring, dst[4];     // this lane's place in a stage, for four rows of words in turn
+    bool one_page;             // the rows of a tile part lie in one page
 
     __device__ __forceinline__ PdStream(const PagedGeom &g, const PdArgs &args, const PdWalk &w,
                                         int64_t tiles, int u, uint32_t ring_addr)
-        : geo(g), a(args), at(w), n(tiles), units(u), ring(ring_addr)
+        : geo(g), a(args), at(w), left(tiles), units(u), ring(ring_addr)
     {
-        key_of_lane = int(threadIdx.x >> 5) * KT + int(threadIdx.x & 31);
+        const int lane = threadIdx.x & 31;
+        key_of_lane = int(threadIdx.x >> 5) * KT + lane;
+        one_page = (1 << g.page_shift) >= KT;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = i * (32 / LPR) + lane / LPR, c = lane % LPR;
+            dst[i] = uint32_t(r * RB + (SWIZZLE ? c ^ (r & 7) : c) * 16);
+        }
         look_up();
     }
     __device__ __forceinline__ bool mine(int key) const
@@ -85,24 +95,41 @@ template <typename T, int D, bool SWIZZLE> struct PdStream {
     // Issue the next tile's copies (none past the end); one group either way.
     __device__ __forceinline__ void load()
     {
-        if (loaded < n) {
+        if (left > 0) {
             const int lane = threadIdx.x & 31, key = at.tile * TILE + key_of_lane;
-            int64_t off = -1;
-            if (mine(key)) {
-                off = key_row(geo, id, at.u / a.chunks, key, D);
-                if (off < 0) report_status(a.ws, REATT_EPAGE);
-            }
-            const uint32_t st = ring + uint32_t(loaded % kPdStages) * kPdStage;
+            const uint32_t st = ring + uint32_t(slot) * kPdStage;
+            const uint8_t *kp = static_cast<const uint8_t *>(a.k_pages);
+            const uint8_t *vp = static_cast<const uint8_t *>(a.v_pages);
+            if (one_page && key - lane + KT <= at.len && uint32_t(__shfl_sync(0xffffffffu, id, 0)) < geo.n_pages) {
+                // all rows there and contiguous: every lane's words lie 512 bytes apart
+                const int64_t first = key_row(geo, __shfl_sync(0xffffffffu, id, 0), at.u / a.chunks,
+                                              key - lane, D) * int64_t(sizeof(T)) + lane * 16;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = i * (32 / LPR) + lane / LPR, c = lane % LPR;
-                const int64_t o = __shfl_sync(0xffffffffu, off, r);
-                const uint32_t dst = st + uint32_t(r * RB + (SWIZZLE ? c ^ (r & 7) : c) * 16);
-                const int64_t src = (o < 0 ? 0 : o) * int64_t(sizeof(T)) + c * 16;
-                cp_async16(dst, static_cast<const uint8_t *>(a.k_pages) + src, o >= 0);
-                cp_async16(dst + kPdHalf, static_cast<const uint8_t *>(a.v_pages) + src, o >= 0);
+                for (int i = 0; i < 8; ++i) {
+                    // rows four instructions apart differ by a multiple of eight, or the
+                    // words are not swizzled by rows that far apart
+                    const uint32_t d = st + dst[i & 3] + uint32_t((i >> 2) * 2048);
+                    cp_async16(d, kp + first + i * 512, true);
+                    cp_async16(d + kPdHalf, vp + first + i * 512, true);
+                }
+            } else {
+                int64_t off = -1;
+                if (mine(key)) {
+                    off = key_row(geo, id, at.u / a.chunks, key, D);
+                    if (off < 0) report_status(a.ws, REATT_EPAGE);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = i * (32 / LPR) + lane / LPR;
+                    const int64_t o = __shfl_sync(0xffffffffu, off, r);
+                    const uint32_t d = st + dst[i & 3] + uint32_t((i >> 2) * 2048);
+                    const int64_t src = (o < 0 ? 0 : o) * int64_t(sizeof(T)) + (lane % LPR) * 16;
+                    cp_async16(d, kp + src, o >= 0);
+                    cp_async16(d + kPdHalf, vp + src, o >= 0);
+                }
             }
-            if (++loaded < n) {
+            slot = slot + 1 == kPdStages ? 0 : slot + 1;
+            if (--left > 0) {
                 at.next<TILE>(geo, a.lens, units);
                 look_up();
             }
@@ -127,7 +154,8 @@ __device__ __forceinline__ void pd_empty(const PagedGeom &geo, const PdArgs &a)
 
 // Joins the warps' (m, l, o) of a unit's part, which they have left in red_ml and
 // red_o, and finishes the unit or leaves the part for the join kernel.  Every thread
-// of the CTA calls it after a barrier, and passes another one after it.
+// of the CTA calls it after a barrier, and passes another one before it writes there
+// again.
 template <typename T, int D, int HB>
 __device__ __forceinline__ void pd_finish(const PagedGeom &geo, const PdArgs &a, const PdWalk &w,
                                           bool begins, bool ends, const float2 (*red_ml)[HB],
@@ -200,6 +228,7 @@ paged_decode_f32_kernel(PagedGeom geo, PdArgs a)
     float qv[HB][E], o[HB][E], m = -INFINITY, l = 0.f;   // m, l: of head lane % HB
     bool fresh = true;
     bool begins = cw.tile == 0;   // this part of the unit starts at its first key
+    int slot = 0;
     for (int64_t i = 0; i < n; ++i) {
         const int h = cw.u / a.chunks, j0 = (cw.u % a.chunks) * HB;   // first query head of the unit
         const int nh = min(HB, geo.g - j0);
@@ -220,7 +249,7 @@ paged_decode_f32_kernel(PagedGeom geo, PdArgs a)
         stream.load();
         cp_async_wait<kPdStages - 1>();
         __syncwarp();
-        const float *kt = reinterpret_cast<const float *>(ring + (i % kPdStages) * kPdStage);
+        const float *kt = reinterpret_cast<const float *>(ring + slot * kPdStage);
         const float *vt = kt + kPdHalf / 4;
         const int key0 = cw.tile * TILE + warp * KT;
         float x[NB];
@@ -283,11 +312,13 @@ paged_decode_f32_kernel(PagedGeom geo, PdArgs a)
             }
         }
         __syncwarp();   // the stage may be refilled
+        slot = slot + 1 == kPdStages ? 0 : slot + 1;
         const bool unit_end = cw.tile + 1 == cw.nt;
         if (unit_end || i + 1 == n) {
             // join the warps, then finish the unit or leave it for the join kernel
 #pragma unroll
             for (int w = HB; w < 32; w <<= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+            __syncthreads();   // the last part's sums have been read
             if (lane < HB) red_ml[warp][lane] = make_float2(m, l);
 #pragma unroll
             for (int j = 0; j < HB; ++j)
@@ -295,7 +326,6 @@ paged_decode_f32_kernel(PagedGeom geo, PdArgs a)
                 for (int e = 0; e < E; ++e) red_o[(warp * HB + j) * D + lane * E + e] = o[j][e];
             __syncthreads();
             pd_finish<float, D, HB>(geo, a, cw, begins, unit_end, red_ml, red_o);
-            __syncthreads();
             fresh = begins = true;
         }
         if (i + 1 < n) cw.next<TILE>(geo, a.lens, units);
@@ -371,50 +401,78 @@ paged_decode_bf16_kernel(PagedGeom geo, PdArgs a)
 
     uint32_t q[HT][D / 16][2];
     float o[HT][D / 16][4], m[HT][2], l[HT][2];   // of heads 8 ht + 2 tc, + 1
-    bool fresh = true;
-    bool begins = cw.tile == 0;   // this part of the unit starts at its first key
-    for (int64_t i = 0; i < n; ++i) {
-        if (fresh) {
-            const int h = cw.u / a.chunks, j0 = (cw.u % a.chunks) * HB, nh = min(HB, geo.g - j0);
+    auto load_q = [&](const PdWalk &w) {
+        const int h = w.u / a.chunks, j0 = (w.u % a.chunks) * HB, nh = min(HB, geo.g - j0);
 #pragma unroll
-            for (int t = 0; t < HT; ++t) {
-                const bool in = 8 * t + gr < nh;
-                const uint32_t *src = reinterpret_cast<const uint32_t *>(
-                    static_cast<const uint16_t *>(a.q) + int64_t(cw.b) * geo.qs +
-                    int64_t(h * geo.g + j0 + (in ? 8 * t + gr : 0)) * D);
+        for (int t = 0; t < HT; ++t) {
+            const bool in = 8 * t + gr < nh;
+            const uint32_t *src = reinterpret_cast<const uint32_t *>(
+                static_cast<const uint16_t *>(a.q) + int64_t(w.b) * geo.qs +
+                int64_t(h * geo.g + j0 + (in ? 8 * t + gr : 0)) * D);
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    q[t][ks][0] = in ? src[ks * 8 + tc] : 0u;
-                    q[t][ks][1] = in ? src[ks * 8 + 4 + tc] : 0u;
-                }
-#pragma unroll
-                for (int dt = 0; dt < D / 16; ++dt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[t][dt][e] = 0.f;
-                m[t][0] = m[t][1] = -INFINITY;
-                l[t][0] = l[t][1] = 0.f;
+            for (int ks = 0; ks < D / 16; ++ks) {
+                q[t][ks][0] = in ? src[ks * 8 + tc] : 0u;
+                q[t][ks][1] = in ? src[ks * 8 + 4 + tc] : 0u;
             }
-            fresh = false;
         }
+    };
+    auto reset = [&] {
+#pragma unroll
+        for (int t = 0; t < HT; ++t) {
+#pragma unroll
+            for (int dt = 0; dt < D / 16; ++dt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[t][dt][e] = 0.f;
+            m[t][0] = m[t][1] = -INFINITY;
+            l[t][0] = l[t][1] = 0.f;
+        }
+    };
+    load_q(cw);
+    reset();
+    bool begins = cw.tile == 0;   // this part of the unit starts at its first key
+    int slot = 0;
+    for (int64_t i = 0; i < n; ++i) {
         stream.load();
         cp_async_wait<kPdStages - 1>();
         __syncwarp();
-        const uint32_t kt = ring + uint32_t(i % kPdStages) * kPdStage, vt = kt + kPdHalf;
+        const uint32_t kt = ring + uint32_t(slot) * kPdStage, vt = kt + kPdHalf;
         const int key0 = cw.tile * TILE + warp * KT;
         float x[KG][HT][4];
 #pragma unroll
         for (int kg = 0; kg < KG; ++kg) {
+            // two chains of products each, added at the end
+            float y[HT][4];
 #pragma unroll
             for (int t = 0; t < HT; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[kg][t][e] = 0.f;
+                for (int e = 0; e < 4; ++e) x[kg][t][e] = y[t][e] = 0.f;
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
                 uint32_t f[4];
                 ldmatrix4<false>(f, kt + uint32_t(kg * 16 * RB) + k_row + (((2 * ks + k_word) ^ swz) << 4));
 #pragma unroll
-                for (int t = 0; t < HT; ++t) mma16816(x[kg][t], f, q[t][ks][0], q[t][ks][1]);
+                for (int t = 0; t < HT; ++t) mma16816(ks & 1 ? y[t] : x[kg][t], f, q[t][ks][0], q[t][ks][1]);
             }
+#pragma unroll
+            for (int t = 0; t < HT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[kg][t][e] = (x[kg][t][e] + y[t][e]) * a.scale;
+        }
+        // the last product with this unit's q: the next one's is on its way meanwhile
+        const bool unit_end = cw.tile + 1 == cw.nt, part_end = unit_end || i + 1 == n;
+        PdWalk nw = cw;
+        if (i + 1 < n) {
+            nw.next<TILE>(geo, a.lens, units);
+            if (part_end) load_q(nw);
+        }
+        if (key0 + KT > cw.len) {
+#pragma unroll
+            for (int kg = 0; kg < KG; ++kg)
+#pragma unroll
+                for (int t = 0; t < HT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (key0 + kg * 16 + gr + (e >> 1) * 8 >= cw.len) x[kg][t][e] = -INFINITY;
         }
         bool lift = false;
 #pragma unroll
@@ -422,11 +480,7 @@ paged_decode_bf16_kernel(PagedGeom geo, PdArgs a)
 #pragma unroll
             for (int t = 0; t < HT; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int key = key0 + kg * 16 + gr + (e >> 1) * 8;
-                    x[kg][t][e] = key < cw.len ? x[kg][t][e] * a.scale : -INFINITY;
-                    lift |= x[kg][t][e] > m[t][e & 1] + kPdMove;
-                }
+                for (int e = 0; e < 4; ++e) lift |= x[kg][t][e] > m[t][e & 1] + kPdMove;
         if (__any_sync(0xffffffffu, lift)) {
 #pragma unroll
             for (int t = 0; t < HT; ++t)
@@ -447,6 +501,12 @@ paged_decode_bf16_kernel(PagedGeom geo, PdArgs a)
                     }
                 }
         }
+        // before any maximum is known every logit is -inf, which has no weight
+        float ref[HT][2];
+#pragma unroll
+        for (int t = 0; t < HT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) ref[t][e] = m[t][e] == -INFINITY ? 0.f : m[t][e];
 #pragma unroll
         for (int kg = 0; kg < KG; ++kg) {
             uint32_t p[HT][2];
@@ -454,8 +514,7 @@ paged_decode_bf16_kernel(PagedGeom geo, PdArgs a)
             for (int t = 0; t < HT; ++t) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    // a masked key is -inf (also before any maximum is known): no weight
-                    const float w = x[kg][t][e] == -INFINITY ? 0.f : pd_ex2(x[kg][t][e] - m[t][e & 1]);
+                    const float w = pd_ex2(x[kg][t][e] - ref[t][e & 1]);
                     l[t][e & 1] += w;
                     x[kg][t][e] = w;
                 }
@@ -474,9 +533,10 @@ paged_decode_bf16_kernel(PagedGeom geo, PdArgs a)
             }
         }
         __syncwarp();   // the stage may be refilled
-        const bool unit_end = cw.tile + 1 == cw.nt;
-        if (unit_end || i + 1 == n) {
+        slot = slot + 1 == kPdStages ? 0 : slot + 1;
+        if (part_end) {
             // join the warps, then finish the unit or leave it for the join kernel
+            __syncthreads();   // the last part's sums have been read
 #pragma unroll
             for (int t = 0; t < HT; ++t)
 #pragma unroll
@@ -493,53 +553,123 @@ paged_decode_bf16_kernel(PagedGeom geo, PdArgs a)
                 }
             __syncthreads();
             pd_finish<uint16_t, D, HB>(geo, a, cw, begins, unit_end, red_ml, red_o);
-            __syncthreads();
-            fresh = begins = true;
+            begins = true;
+            reset();
         }
-        if (i + 1 < n) cw.next<TILE>(geo, a.lens, units);
+        cw = nw;
     }
     cp_async_wait<0>();
 }
 
 // The join: block i finishes the unit that begins in range i and goes on in the
-// following ranges, from its partials in order.
+// following ranges.  Every partial's weight is formed once; then groups of threads
+// take every kJoinGroups-th partial, four elements a thread with several loads in
+// flight, and the groups' sums are added in order.
+constexpr int kJoinThreads = 512, kJoinParts = 64;
 template <typename T, int D, int HB>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kJoinThreads)
 paged_decode_join_kernel(PagedGeom geo, PdArgs a)
 {
+    constexpr int WORDS = HB * D / 4;                  // float4 words of a partial
+    constexpr int GROUPS = WORDS >= kJoinThreads ? 1 : kJoinThreads / WORDS;
+    constexpr int PER = WORDS <= kJoinThreads ? 1 : WORDS / kJoinThreads;
     __shared__ int last_s;
-    pdl_wait();
-    const PdMeta me = a.meta[blockIdx.x];
-    if (me.open_b < 0) return;
-    // the range that ends the unit: the first one after this whose slot says so
-    const int tid = threadIdx.x, n = gridDim.x;
+    __shared__ float top[HB], total[HB], weight[kJoinParts][HB];
+    __shared__ float4 sums[GROUPS > 1 ? GROUPS : 1][GROUPS > 1 ? WORDS : 1];
+    const int tid = threadIdx.x, n = gridDim.x, first = blockIdx.x;
     if (tid == 0) last_s = n - 1;
+    pdl_wait();
     __syncthreads();
-    for (int i = blockIdx.x + 1 + tid; i < n; i += 256)
+    // the range that ends the unit: the first one after this whose slot says so
+    const PdMeta me = a.meta[first];
+    for (int i = first + 1 + tid; i < n; i += kJoinThreads)
         if (a.meta[i].first == 1) atomicMin(&last_s, i);
+    if (me.open_b < 0) return;
     __syncthreads();
-    const int last = last_s;
+    const int parts = last_s - first + 1;
+    // partial x is range first + x's: its last slot for x = 0, else its first one
+    auto slot_of = [&](int x) { return x == 0 ? 2 * first + 1 : 2 * (first + x); };
     const int h = me.open_u / a.chunks, j0 = (me.open_u % a.chunks) * HB;
     const int nh = min(HB, geo.g - j0);
-    for (int y = tid; y < nh * D; y += 256) {
-        const int j = y / D, c = y - j * D;
-        const int first = 2 * blockIdx.x + 1;
-        float M = a.part_ml[first * HB + j].x;
-        for (int i = blockIdx.x + 1; i <= last; ++i) M = fmaxf(M, a.part_ml[2 * i * HB + j].x);
-        float2 ml = a.part_ml[first * HB + j];
-        float f = pd_weight(ml.x, M);
-        float L = f * ml.y, acc = f * a.part_acc[(int64_t(first) * HB + j) * D + c];
-        for (int i = blockIdx.x + 1; i <= last; ++i) {
-            ml = a.part_ml[2 * i * HB + j];
-            f = pd_weight(ml.x, M);
-            L += f * ml.y;
-            acc += f * a.part_acc[(int64_t(2 * i) * HB + j) * D + c];
+    // the joint maximum and sum of each head, a warp per head
+    for (int j = tid >> 5; j < nh; j += kJoinThreads / 32) {
+        const int lane = tid & 31;
+        float M = -INFINITY, L = 0.f;
+        for (int x = lane; x < parts; x += 32) {
+            const float2 ml = a.part_ml[slot_of(x) * HB + j];
+            const float mn = fmaxf(M, ml.x);
+            L = L * pd_weight(M, mn) + pd_weight(ml.x, mn) * ml.y;
+            M = mn;
         }
-        store_elem(static_cast<T *>(a.out) + (int64_t(me.open_b) * geo.Hq + h * geo.g + j0 + j) * D + c,
-                   acc / L);
+        float top_m = M;
+#pragma unroll
+        for (int w = 16; w; w >>= 1) top_m = fmaxf(top_m, __shfl_xor_sync(0xffffffffu, top_m, w));
+        L *= pd_weight(M, top_m);
+#pragma unroll
+        for (int w = 16; w; w >>= 1) L += __shfl_xor_sync(0xffffffffu, L, w);
+        if (lane == 0) {
+            top[j] = top_m;
+            total[j] = L;
+        }
+    }
+    float4 acc[PER];
+#pragma unroll
+    for (int r = 0; r < PER; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int group = PER > 1 ? 0 : tid / WORDS;
+    for (int x0 = 0; x0 < parts; x0 += kJoinParts) {
+        const int np = min(kJoinParts, parts - x0);
+        __syncthreads();
+        for (int y = tid; y < np * HB; y += kJoinThreads) {
+            const int x = y / HB, j = y - x * HB;
+            weight[x][j] = j < nh ? pd_weight(a.part_ml[slot_of(x0 + x) * HB + j].x, top[j]) : 0.f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < PER; ++r) {
+            const int word = PER > 1 ? r * kJoinThreads + tid : tid % WORDS, j = word * 4 / D;
+            if (j < nh && group < GROUPS) {
+#pragma unroll 8
+                for (int x = group; x < np; x += GROUPS) {
+                    const float4 v = reinterpret_cast<const float4 *>(
+                        a.part_acc + int64_t(slot_of(x0 + x)) * HB * D)[word];
+                    const float f = weight[x][j];
+                    acc[r].x = fmaf(f, v.x, acc[r].x);
+                    acc[r].y = fmaf(f, v.y, acc[r].y);
+                    acc[r].z = fmaf(f, v.z, acc[r].z);
+                    acc[r].w = fmaf(f, v.w, acc[r].w);
+                }
+            }
+        }
+    }
+    if constexpr (GROUPS > 1) {
+        sums[group][tid % WORDS] = acc[0];
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int i = 1; i < GROUPS; ++i) {
+            const float4 v = sums[i][tid];
+            acc[0].x += v.x;
+            acc[0].y += v.y;
+            acc[0].z += v.z;
+            acc[0].w += v.w;
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < PER; ++r) {
+        const int word = PER > 1 ? r * kJoinThreads + tid : tid % WORDS;
+        const int j = word * 4 / D, c = word * 4 - j * D;
+        if (j < nh) {
+            T *dst = static_cast<T *>(a.out) + (int64_t(me.open_b) * geo.Hq + h * geo.g + j0 + j) * D + c;
+            const float il = 1.f / total[j];
+            store_elem(dst, acc[r].x * il);
+            store_elem(dst + 1, acc[r].y * il);
+            store_elem(dst + 2, acc[r].z * il);
+            store_elem(dst + 3, acc[r].w * il);
+        }
     }
 }
 
+constexpr int kPdResident = 2;   // CTAs of an SM, at most
 constexpr int kMaxHeads = 16;   // query heads of a unit, at most
 
 template <typename T, int D, int HB>
@@ -548,12 +678,12 @@ cudaError_t run(void (*kern)(PagedGeom, PdArgs), const PagedGeom &g, PdArgs a, c
     a.chunks = (g.g + HB - 1) / HB;
     const size_t smem = size_t(kPdWarps) * kPdStages * kPdStage + size_t(kPdWarps) * HB * D * 4;
     // one range per CTA that the SMs hold at once
-    const int ranges = num_sms() * (2 * (smem + 2048) <= 228 * 1024 ? 2 : 1);
+    const int ranges = num_sms() * int(std::min<size_t>(kPdResident, 228 * 1024 / (smem + 2048)));
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, dim3(unsigned(ranges)), dim3(kPdThreads), smem, st, g, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(paged_decode_join_kernel<T, D, HB>, dim3(unsigned(ranges)), dim3(256), 0, st, g, a);
+    return launch_pdl(paged_decode_join_kernel<T, D, HB>, dim3(unsigned(ranges)), dim3(kJoinThreads), 0, st, g, a);
 }
 // Query heads of a unit: as few as hold the group, at most 8 (fp32, whose products
 // cost an instruction each) or 16.
@@ -566,7 +696,7 @@ template <int D> cudaError_t run_d(const PagedGeom &g, const PdArgs &a, cudaStre
                     : run<float, D, 8>(paged_decode_f32_kernel<D, 8>, g, a, st);
 }
 
-int max_ranges() { return 2 * num_sms(); }
+int max_ranges() { return kPdResident * num_sms(); }
 
 }  // namespace
 

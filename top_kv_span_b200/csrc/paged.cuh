@@ -17,7 +17,7 @@ struct PagedGeom {
     int64_t qs, ks, vs;  // elements between the packed rows of q, k, v
     int64_t qrs, krs;    // the same of the rotated copies
     bool rotate;         // rope_base != 0
-    float rope_hi[64];   // RoPE frequencies in half-turns, hi + lo (see rope_cs)
+    float rope_hi[64];   // append: RoPE frequencies in half-turns, hi + lo (see rope_cs)
     float rope_lo[64];
 
     // tokens that a sequence's row of the page table can hold

@@ -157,6 +157,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     const int TPT = kPtRows / geo.g, TB = 2 * TPT;   // tokens of a tile, of the block
     const int h = blockIdx.x % geo.Hkv;
     if (warp == kPtSoft) {
+        if (lane < 3) prefetch_tensormap(lane == 0 ? &qmap : lane == 1 ? &kmap : &vmap);
         const PromptBlock r = prompt_block(geo, cu, TB, blockIdx.x / geo.Hkv);
         if (lane == 0) sh.blk = r;
     } else if (warp == kPtSoft + 3) {

@@ -5,7 +5,8 @@
 // A row is one (token, query head) pair of a KV head, heads innermost, so the g
 // query heads of a token lie in one tile and a K/V tile is read once for all of
 // them.  A block is two tiles of floor(128 / g) tokens each (TMEM lanes = rows) of one
-// KV head.  One CTA per SM walks its share of the blocks, the long ones first, and
+// KV head.  A CTA per SM takes one block after another (claiming the
+// places of CTAs that have not started), the long ones first, and
 // each block's keys 64 at a time (a step), S = Q.K^T and O += P.V as products of
 // M = 128 and N = 64 or d, with the running maximum and sum of the softmax:
 //   warps 0-3, 4-7  softmax of tile 0, 1: a thread owns a row; it reads its S
@@ -13,7 +14,7 @@
 //            rescales its row of O in TMEM) only when the row's maximum grows by
 //            more than 2^8, and writes P = 2^(x - m) as bf16 over its own S; at the
 //            block's end it divides its row of O by the sum and stores it
-//   warp 8   finds the blocks, and loads by TMA: Q as soon as the last block's S
+//   warp 8   claims and finds the blocks, and loads by TMA: Q as soon as the last block's S
 //            products have read theirs, and a ring of pairs, first {K(0), K(1)}, then
 //            {V(s), K(s+2)}, that runs on from block to block
 //   warps 9, 10  issue one tile's products each, P(s).V(s) and then
@@ -67,7 +68,10 @@ struct PtShared {
     uint64_t done[2], oempty[2];            // the block's O complete, read
     uint64_t last[2];                       // all products complete
     uint64_t turn[2];                       // a step's exponentials half done
+    uint64_t claim;                         // the next block's index has come
     PromptBlock blk[2];
+    int head[2];                            // its KV head
+    alignas(16) uint8_t claimed[16];
     uint32_t tmem;
     int abort_flag;
     int odd[4];                             // block (mod 4) whose V had infinities or NaN, + 1
@@ -136,6 +140,30 @@ __device__ __forceinline__ void tmem_st16_nowait(uint32_t taddr, const uint32_t 
         : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Cluster launch control: asks for a CTA of this grid that has not started; the 16-byte
+// answer lands in shared memory and completes the mbarrier's transaction.
+__device__ __forceinline__ void claim_cta(void *answer, uint64_t *bar)
+{
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_addr(answer)),
+                 "r"(smem_addr(bar))
+                 : "memory");
+}
+// The claimed CTA's index, which will not start by itself, or -1: none was left.
+__device__ __forceinline__ int claimed_cta(const void *answer)
+{
+    uint32_t got, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
+        "ld.shared.b128 h, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+        : "=r"(got), "=r"(x)
+        : "r"(smem_addr(answer))
+        : "memory");
+    return got ? int(x) : -1;
+}
 // One lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one()
 {
@@ -153,7 +181,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap vmap, PagedGeom geo,
                  const int32_t *__restrict__ cu, const uint16_t *__restrict__ v,
-                 uint16_t *__restrict__ out, int total, float scale, void *ws)
+                 uint16_t *__restrict__ out, float scale, void *ws)
 {
     using Sm = PtSmem<D>;
     constexpr int NS = Sm::kStages, NBOX = Sm::NBOX;
@@ -173,6 +201,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         sh.abort_flag = 0;
         for (int i = 0; i < 4; ++i) sh.odd[i] = 0;
         mbar_init(&sh.qfull, 1);
+        mbar_init(&sh.claim, 1);
         mbar_init(&sh.qempty, 2);
         for (int r = 0; r < NS; ++r) {
             mbar_init(&sh.full[r], 1);
@@ -214,12 +243,6 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             if ((i & 1023) == 0 && (aborted() || i >= (1 << 26))) return false;
         return true;
     };
-    // the k-th block of this CTA: forth and back through the list, which is in
-    // descending order of work, so that the shares are even
-    auto place = [&](int k) {
-        const int64_t i = int64_t(k) * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        return i < total ? int(i) : -1;
-    };
     struct Block {
         int begin, len, q0, h;   // the sequence's first row and length, first token, KV head
         int rows0, rows1;        // tokens of each tile and its steps (none past the
@@ -228,7 +251,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         __device__ int rows(int t) const { return t ? rows1 : rows0; }
         __device__ int n(int t) const { return t ? n1 : n0; }
     };
-    auto block_of = [&](const PromptBlock &p, int k) {
+    auto block_of = [&](const PromptBlock &p, int h) {
         auto rows_of = [&](int t) { return max(0, min(TPT, p.len - p.q0 - t * TPT)); };
         auto steps = [&](int t, int rows) {
             return rows ? (p.q0 + t * TPT + rows + kPtKeys - 1) / kPtKeys : 0;
@@ -238,7 +261,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         b.begin = p.begin;
         b.len = p.len;
         b.q0 = p.q0;
-        b.h = place(k) % geo.Hkv;
+        b.h = h;
         b.rows0 = rows_of(0);
         b.rows1 = rows_of(1);
         b.n0 = steps(0, b.rows0);
@@ -250,11 +273,15 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     auto next_block = [&](int k) {
         const bool got = __all_sync(0xffffffffu, poll(&sh.info_full[k & 1], k >> 1));
         PromptBlock p{0, 0, 0, false};
-        if (got) p = sh.blk[k & 1];
+        int h = 0;
+        if (got) {
+            p = sh.blk[k & 1];
+            h = sh.head[k & 1];
+        }
         __syncwarp();
         if (got && lane == 0) mbar_arrive(&sh.info_empty[k & 1]);
         if (!got && lane == 0) fail();
-        return block_of(p, k);
+        return block_of(p, h);
     };
 
     // registers move from the four service warps to the softmax warps:
@@ -265,15 +292,22 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             // ------------------------------------------------ blocks and loads
             int item = 0, loads = 0;   // ring items and Q tiles loaded so far
             bool ok = true;
+            // this CTA's own place in the list of blocks, then those it claims from CTAs
+            // that have not started: the list descends in work, so the SMs end together
+            int i = blockIdx.x;
             for (int k = 0;; ++k) {
-                const int i = place(k);
                 PromptBlock p{0, 0, 0, false};
                 if (i >= 0) p = prompt_block(geo, cu, TB, i / geo.Hkv);
-                const Block b = block_of(p, k);
+                const Block b = block_of(p, i < 0 ? 0 : i % geo.Hkv);
                 if (lane == 0) {
+                    if (b.live) {
+                        mbar_arrive_expect_tx(&sh.claim, 16);
+                        claim_cta(sh.claimed, &sh.claim);
+                    }
                     ok = k < 2 || wait(&sh.info_empty[k & 1], (k >> 1) - 1);
                     if (ok) {
                         sh.blk[k & 1] = p;
+                        sh.head[k & 1] = b.h;
                         mbar_arrive(&sh.info_full[k & 1]);
                     }
                     if (ok && b.live) {
@@ -302,10 +336,16 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                             }
                         }
                     }
+                    if (b.live) {
+                        ok = wait(&sh.claim, k) && ok;
+                        i = claimed_cta(sh.claimed);
+                        fence_proxy_async_smem();   // read before the next claim is answered there
+                    }
                     if (!ok) fail();
                 }
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok || !b.live) break;
+                i = __shfl_sync(0xffffffffu, i, 0);
             }
             if (lane == 0) {
                 // the copies in flight land before the CTA may leave
@@ -670,14 +710,13 @@ cudaError_t run(const PagedGeom &g, const void *q, const void *k, const void *v,
     // every sequence has at most one block that is not full
     const int64_t blocks = (g.N / TB + (g.B < g.N ? g.B : g.N)) * g.Hkv;
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    const unsigned grid = unsigned(blocks < num_sms() ? blocks : num_sms());
     auto kern = prompt_tc_kernel<D>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          int(PtSmem<D>::kBytes));
     if (e != cudaSuccess) return e;
-    kern<<<grid, kPtThreads, PtSmem<D>::kBytes, st>>>(
+    kern<<<unsigned(blocks), kPtThreads, PtSmem<D>::kBytes, st>>>(
         qm, km, vm, g, cu, static_cast<const uint16_t *>(v), static_cast<uint16_t *>(out),
-        int(blocks), float(1.4426950408889634 / sqrt(double(D))), ws);
+        float(1.4426950408889634 / sqrt(double(D))), ws);
     return cudaGetLastError();
 }
 

@@ -41,6 +41,8 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "kernels.h"
 #include "prompt.cuh"
 #include "tc_ptx.cuh"
@@ -470,21 +472,16 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.turn[t]);
             };
-            for (int j = 0; j < b.ns; ++j) {
-                if (j >= n) {
-                    ok = __all_sync(0xffffffffu, my_turn(j));
-                    if (!ok) break;
-                    pass_on();
-                    continue;
-                }
+            // One step; only the edge steps (from s_odd on) hold keys that some row does
+            // not see.  The others have a loop of their own without that code.
+            auto one_step = [&](int j, auto edge) {
                 const int g = step + j;
                 const uint32_t t_s = lanes + kPtS + uint32_t((t * 2 + (g & 1)) * kPtKeys);
-                if (j >= s_odd) {
+                if constexpr (decltype(edge)::value) {
                     // look V(j) over: 16-byte words of this thread; the swizzle only
                     // permutes words within a key's 128-byte row
                     const int it = item + 1 + j, r = it % NS;
-                    ok = __all_sync(0xffffffffu, poll(&sh.full[r], it / NS));
-                    if (!ok) break;
+                    if (!__all_sync(0xffffffffu, poll(&sh.full[r], it / NS))) return false;
                     uint8_t *vt = smem + Sm::oRing + r * Sm::kStage;
                     for (int x = row * 16; x < Sm::kHalf; x += kPtRows * 16) {
                         uint4 *p = reinterpret_cast<uint4 *>(vt + x);
@@ -509,8 +506,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                     }
                     fence_proxy_async_smem();   // before this warp's arrival for P(j)
                 }
-                ok = __all_sync(0xffffffffu, poll(&sh.sfull[t][g & 1], g >> 1));
-                if (!ok) break;
+                if (!__all_sync(0xffffffffu, poll(&sh.sfull[t][g & 1], g >> 1))) return false;
                 tc_fence_after();
                 float s[kPtKeys];
                 {
@@ -525,8 +521,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                         for (int i = 0; i < 32; ++i) s[c * 32 + i] = __uint_as_float(a[c][i]);
                     }
                 }
-                const int k0 = j * kPtKeys;
-                if (k0 + kPtKeys - 1 > lim) {
+                if constexpr (decltype(edge)::value) {
+                    const int k0 = j * kPtKeys;
 #pragma unroll
                     for (int i = 0; i < kPtKeys; ++i)
                         if (k0 + i > lim) s[i] = -INFINITY;
@@ -536,8 +532,9 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
 #pragma unroll
                 for (int i = 0; i < kPtKeys; i += 2) pm[i / 2 & 3] = fmaxf(pm[i / 2 & 3], fmaxf(s[i], s[i + 1]));
                 const float mx = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
-                // the reference stays while no row's maximum has grown by 2^8
-                if (__any_sync(0xffffffffu, !(mx <= m + lift))) {
+                // the reference stays while no row's maximum has grown by 2^8 (rows that do
+                // not exist hold anything and do not count)
+                if (__any_sync(0xffffffffu, live && !(mx <= m + lift))) {
                     const bool first = m == -INFINITY;
                     const bool move = mx != -INFINITY && (first || !(mx <= m + lift));
                     float fac = 1.f;
@@ -549,9 +546,9 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                     if (j > 0 && __any_sync(0xffffffffu, move && !first)) {
                         // O is at rest once P(j-1).V(j-1) is complete, as P(j).V(j) waits for
                         // this P; S(j+1) was issued after it and tells of it
-                        ok = __all_sync(0xffffffffu, j + 1 < n ? poll(&sh.sfull[t][(g + 1) & 1], (g + 1) >> 1)
-                                                               : poll(&sh.odone[t], twos));
-                        if (!ok) break;
+                        if (!__all_sync(0xffffffffu, j + 1 < n ? poll(&sh.sfull[t][(g + 1) & 1], (g + 1) >> 1)
+                                                               : poll(&sh.odone[t], twos)))
+                            return false;
                         tc_fence_after();
 #pragma unroll 1
                         for (int c = 0; c < D; c += 32) {
@@ -565,8 +562,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 }
                 // masked keys are -inf and give 0; without any key yet m is -inf: all give 0
                 const float mc = m == -INFINITY ? 0.f : m * scale;
-                ok = __all_sync(0xffffffffu, my_turn(j));
-                if (!ok) break;
+                if (!__all_sync(0xffffffffu, my_turn(j))) return false;
                 const uint64_t sc2 = pack2(scale, scale), mc2 = pack2(-mc, -mc);
                 uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -594,6 +590,14 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 float l0, l1;
                 unpack2(l2, l0, l1);
                 l += l0 + l1;
+                return true;
+            };
+            int j = 0;
+            for (const int inner = min(n, s_odd); ok && j < inner; ++j) ok = one_step(j, std::false_type());
+            for (; ok && j < n; ++j) ok = one_step(j, std::true_type());
+            for (; ok && j < b.ns; ++j) {   // steps that only the other tile has
+                ok = __all_sync(0xffffffffu, my_turn(j));
+                if (ok) pass_on();
             }
             if (ok && n > 0) {
                 ok = __all_sync(0xffffffffu, poll(&sh.done[t], used));

@@ -37,4 +37,26 @@ __device__ __forceinline__ void packed_rows(const int32_t *__restrict__ cu, int 
     end = max(min(cu[b + 1], n), begin);
 }
 
+// 16 bytes global -> shared without passing registers; fill = false writes zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool fill)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(fill ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// 2^x on the special-function unit (relative error about 2^-22; 2^-inf = 0).
+__device__ __forceinline__ float ex2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 }  // namespace reatt

@@ -290,7 +290,7 @@ paged_decode_f32_kernel(PagedGeom geo, PdArgs a)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             // a masked key is -inf; a row of logits that are all -inf keeps l = 0
-            p[nb] = x[nb] == -INFINITY ? 0.f : pd_ex2(x[nb] - m);
+            p[nb] = x[nb] == -INFINITY ? 0.f : ex2_approx(x[nb] - m);
             ps += p[nb];
         }
         l = l * fac + ps;
@@ -514,7 +514,7 @@ paged_decode_bf16_kernel(PagedGeom geo, PdArgs a)
             for (int t = 0; t < HT; ++t) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float w = pd_ex2(x[kg][t][e] - ref[t][e & 1]);
+                    const float w = ex2_approx(x[kg][t][e] - ref[t][e & 1]);
                     l[t][e & 1] += w;
                     x[kg][t][e] = w;
                 }

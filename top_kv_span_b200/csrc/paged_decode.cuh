@@ -135,31 +135,10 @@ __device__ __forceinline__ int64_t pd_range(const PagedGeom &geo, const int32_t 
     return t1 - t0;
 }
 
-// 2^x on the special-function unit (relative error about 2^-22; 2^-inf = 0).
-__device__ __forceinline__ float pd_ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // Weight of a partial with maximum m under the joint maximum M.
 __device__ __forceinline__ float pd_weight(float m, float M)
 {
-    return m == -INFINITY ? 0.f : pd_ex2(m - M);
-}
-
-// 16 bytes global -> shared without passing registers; fill = false writes zeros.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool fill)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(fill ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+    return m == -INFINITY ? 0.f : ex2_approx(m - M);
 }
 
 }  // namespace reatt

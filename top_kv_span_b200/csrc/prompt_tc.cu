@@ -100,13 +100,6 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, i
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
         : "memory");
 }
-// 2^x on the special-function unit (relative error about 2^-22; 2^-inf = 0).
-__device__ __forceinline__ float pt_ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // Two fp32 values in one 64-bit register and packed arithmetic on them.
 __device__ __forceinline__ uint64_t pack2(float a, float b)
 {
@@ -539,7 +532,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                     const bool move = mx != -INFINITY && (first || !(mx <= m + lift));
                     float fac = 1.f;
                     if (move) {
-                        fac = first ? 0.f : pt_ex2((m - mx) * scale);
+                        fac = first ? 0.f : ex2_approx((m - mx) * scale);
                         m = mx;
                         l *= fac;
                     }
@@ -573,8 +566,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                         const uint64_t x = fma2(pack2(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]), sc2, mc2);
                         float p0, p1;
                         unpack2(x, p0, p1);
-                        p0 = pt_ex2(p0);
-                        p1 = pt_ex2(p1);
+                        p0 = ex2_approx(p0);
+                        p1 = ex2_approx(p1);
                         sum[i & 3] = add2(sum[i & 3], pack2(p0, p1));
                         const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
                         w[i] = *reinterpret_cast<const uint32_t *>(&b2);

@@ -583,3 +583,127 @@ def test_wrong_dtypes_are_refused(R):
     with pytest.raises(R.ReattError):
         R.reatt_prompt_attend(dims, q.to(BF16), q.to(BF16), q.to(BF16),
                               torch.zeros(2, dtype=torch.int64, device="cuda"), q.to(BF16), ws)
+
+
+# ------------------------------------------------------------------ large and concurrent
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_pool_offsets_beyond_32_bits(R, dtype):
+    """Pools of more than 2^32 elements: the tokens sit in the last pages."""
+    Hq, Hkv, d, page, n_pages = 16, 8, 128, 64, 66000      # 4.3e9 elements a pool
+    kp = torch.empty((n_pages, Hkv, page, d), dtype=dtype, device="cuda")
+    vp = torch.empty_like(kp)
+    gen = torch.Generator().manual_seed(41)
+    n = 150
+    x = torch.randn((n, Hq + 2 * Hkv, d), generator=gen).to(dtype)
+    dev = x.cuda()
+    q, k, v = dev[:, :Hq], dev[:, Hq:Hq + Hkv], dev[:, Hq + Hkv:]
+    table = torch.tensor([[n_pages - 1, n_pages - 3, n_pages - 2]], dtype=torch.int32)
+    strides = dict(q_stride=x.stride(0), k_stride=x.stride(0), v_stride=x.stride(0))
+    dims = R.make_paged_dims(B=1, Hq=Hq, Hkv=Hkv, d=d, dtype=dtype, N=n, page=page, max_pages=3,
+                             n_pages=n_pages, **strides)
+    ws, seq = workspace(R, dims), ints([0])
+    R.reatt_paged_append(dims, None, k, v, ints([0, n]), ints([0]), table.cuda(), None, None, kp, vp,
+                         seq, ws)
+    pos = torch.arange(n)
+    where, slot = table[0][pos // page].long().cuda(), (pos % page).cuda()
+    assert torch.equal(kp[where, :, slot], k) and torch.equal(vp[where, :, slot], v)
+    one = R.make_paged_dims(B=1, Hq=Hq, Hkv=Hkv, d=d, dtype=dtype, N=1, page=page, max_pages=3,
+                            n_pages=n_pages, **strides)
+    out = torch.empty((1, Hq, d), dtype=dtype, device="cuda")
+    R.reatt_paged_decode(one, q[n - 1:], kp, vp, table.cuda(), seq, out, ws)
+    torch.cuda.synchronize()
+    assert R.reatt_workspace_status(ws) == R.OK
+    o, tol = ref.attend(x[n - 1:, :Hq].transpose(0, 1), x[:, Hq:Hq + Hkv].transpose(0, 1),
+                        x[:, Hq + Hkv:].transpose(0, 1), torch.tensor([n - 1]))
+    ref.check(out.cpu(), o.transpose(0, 1), tol.transpose(0, 1))
+
+
+@pytest.mark.parametrize("dtype,N", [(BF16, 600_064), (F32, 540_672)])
+def test_prompt_offsets_beyond_31_bits(R, dtype, N):
+    """Packed rows of more than 2^31 elements in q and out; many sequences."""
+    Hq, Hkv, d, n = 32, 2, 128, 128
+    lens = [n] * (N // n - 1) + [n - 5]
+    gen = torch.Generator("cuda").manual_seed(43)
+    q = torch.empty((N, Hq, d), dtype=dtype, device="cuda")
+    k, v = (torch.randn((N, Hkv, d), generator=gen, device="cuda").to(dtype) for _ in range(2))
+    picks = [0, 1, len(lens) // 2, len(lens) - 2, len(lens) - 1]
+    cu = starts(lens)
+    q.zero_()
+    for b in picks:
+        q[cu[b]:cu[b + 1]] = torch.randn((lens[b], Hq, d), generator=gen, device="cuda").to(dtype)
+    dims = R.make_paged_dims(B=len(lens), Hq=Hq, Hkv=Hkv, d=d, dtype=dtype, N=N)
+    out = torch.empty_like(q)
+    ws = workspace(R, dims)
+    R.reatt_prompt_attend(dims, q, k, v, ints(cu), out, ws)
+    torch.cuda.synchronize()
+    assert R.reatt_workspace_status(ws) == R.OK
+    for b in picks:
+        r = slice(cu[b], cu[b + 1])
+        o, tol = ref.attend(*(t[r].cpu().transpose(0, 1) for t in (q, k, v)), torch.arange(lens[b]))
+        ref.check(out[r].cpu(), o.transpose(0, 1), tol.transpose(0, 1), f"sequence {b}")
+
+
+def test_calls_on_two_streams_at_once(R):
+    """Prompt attention and decode on two streams, each with its own workspace, many
+    times over: every result equals the one alone."""
+    gen = torch.Generator().manual_seed(51)
+    lens = [700, 90, 1300]
+    N = sum(lens)
+    q, k, v = (torch.randn((N, h, 128), generator=gen).to(BF16).cuda() for h in (8, 2, 2))
+    pd = R.make_paged_dims(B=3, Hq=8, Hkv=2, d=128, dtype=BF16, N=N)
+    cu = ints(starts(lens))
+    pool = ref.Pool([4000, 77, 900], 2, 128, 32, BF16, 5)
+    dd = R.make_paged_dims(B=3, Hq=8, Hkv=2, d=128, dtype=BF16, N=3, page=32,
+                           max_pages=pool.max_pages, n_pages=pool.n_pages)
+    dq = torch.randn((3, 8, 128), generator=gen).to(BF16).cuda()
+    args = (dq, pool.k.cuda(), pool.v.cuda(), pool.table.cuda(), ints([4000, 77, 900]))
+    w = [workspace(R, pd), workspace(R, pd), workspace(R, dd), workspace(R, dd)]
+    want_p, want_d = torch.empty_like(q), torch.empty_like(dq)
+    R.reatt_prompt_attend(pd, q, k, v, cu, want_p, w[0])
+    R.reatt_paged_decode(dd, *args, want_d, w[2])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    outs = [[torch.full_like(want_p if i < 2 else want_d, math.nan) for _ in range(10)] for i in range(4)]
+    torch.cuda.synchronize()
+    for j in range(10):
+        for i, s in enumerate(streams):
+            if i < 2:
+                R.reatt_prompt_attend(pd, q, k, v, cu, outs[i][j], w[i], stream=s)
+            else:
+                R.reatt_paged_decode(dd, *args, outs[i][j], w[i], stream=s)
+    torch.cuda.synchronize()
+    for i in range(4):
+        for o in outs[i]:
+            assert torch.equal(o, want_p if i < 2 else want_d)
+        assert R.reatt_workspace_status(w[i]) == R.OK
+
+
+def test_prompt_captured_with_lengths_that_change(R):
+    """Offsets are read when the kernel runs: one captured call, replayed with other
+    offsets in the same buffer."""
+    for dtype in (BF16, F32):
+        gen = torch.Generator().manual_seed(61)
+        N = 900
+        x = [torch.randn((N, h, 64), generator=gen).to(dtype) for h in (6, 2, 2)]
+        q, k, v = (t.cuda() for t in x)
+        dims = R.make_paged_dims(B=4, Hq=6, Hkv=2, d=64, dtype=dtype, N=N)
+        cu, ws = ints([0, 0, 0, 0, 0]), workspace(R, dims)
+        out = torch.empty_like(q)
+        R.reatt_prompt_attend(dims, q, k, v, cu, out, ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            R.reatt_prompt_attend(dims, q, k, v, cu, out, ws)
+        for lens in ([900, 0, 0, 0], [1, 400, 99, 400], [0, 0, 30, 200], [0, 0, 0, 0]):
+            cu.copy_(ints(starts(lens)))
+            out.fill_(5.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            at = 0
+            for n in lens:
+                if n:
+                    o, tol = ref.attend(*(t[at:at + n].transpose(0, 1) for t in x), torch.arange(n))
+                    ref.check(out[at:at + n].cpu(), o.transpose(0, 1), tol.transpose(0, 1))
+                at += n
+            assert (out[at:] == 5.0).all()
+        assert R.reatt_workspace_status(ws) == R.OK

@@ -309,24 +309,24 @@ def make_paged_dims(B, Hq, Hkv, d, dtype, N, page=1, max_pages=1, n_pages=1, rop
                             int(v_stride), int(q_rot_stride), int(k_rot_stride), float(rope_base))
 
 
-def _paged_check(where, code, data, ints, ws):
-    """What the library cannot see of a paged call's tensors: each lives on the
-    current device and has the dtype of the dims (int32 for lengths and tables).
-    Addresses (int) and None pass."""
-    want = torch.bfloat16 if code == BF16 else torch.float32
-    dev = None
+def _paged_args(where, code, data, ints, ws):
+    """Device addresses of a paged call's tensors: data, ints, ws.  What the library
+    cannot see is checked on the way: each tensor lives on the current device and has
+    the dtype of the dims (int32 for lengths and tables).  Addresses (int) and None
+    pass."""
+    want, dev, out = (torch.bfloat16 if code == BF16 else torch.float32), None, []
     for group, dt in ((data, want), (ints, torch.int32), ((ws,), None)):
         for t in group:
-            if t is None or isinstance(t, int):
+            if t is None or t.__class__ is int:
+                out.append(t)
                 continue
-            d = t.get_device()
-            if d == dev and (t.dtype is dt or dt is None):
-                continue
-            if dev is None and d >= 0:
+            if dev is None and t.is_cuda:
                 dev = torch.cuda.current_device()
-            if d != dev or not (t.dtype is dt or dt is None):
+            if t.get_device() != dev or (t.dtype is not dt and dt is not None):
                 raise ReattError(EINVAL, f"{where}: a tensor of {t.dtype} on {t.device}, wanted "
                                          f"{dt or 'any dtype'} on the current CUDA device")
+            out.append(t.data_ptr())
+    return out
 
 
 def reatt_paged_workspace_bytes(dims) -> int:
@@ -340,12 +340,11 @@ def reatt_paged_append(dims, q, k, v, cu_seqlens, past_len, page_table, q_rot, k
                        v_pages, seq_len, ws, stream=None, check=True):
     """Append packed new tokens to the paged caches, k (and q) rotated at their
     positions; q/q_rot, k_rot and seq_len may be None."""
-    _paged_check("reatt_paged_append", dims.dtype, (k, v, k_pages, v_pages, q, q_rot, k_rot),
-                 (cu_seqlens, past_len, page_table, seq_len), ws)
-    rc = lib.reatt_paged_append(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens),
-                                _ptr(past_len), _ptr(page_table), _ptr(q_rot), _ptr(k_rot),
-                                _ptr(k_pages), _ptr(v_pages), _ptr(seq_len), _ptr(ws),
-                                _stream(stream))
+    pk, pv, pkp, pvp, pq, pqr, pkr, pcu, ppast, ptab, plen, pws = _paged_args(
+        "reatt_paged_append", dims.dtype, (k, v, k_pages, v_pages, q, q_rot, k_rot),
+        (cu_seqlens, past_len, page_table, seq_len), ws)
+    rc = lib.reatt_paged_append(ctypes.byref(dims), pq, pk, pv, pcu, ppast, ptab, pqr, pkr, pkp,
+                                pvp, plen, pws, _stream(stream))
     if check:
         _check(rc, "reatt_paged_append")
     return rc
@@ -354,10 +353,9 @@ def reatt_paged_append(dims, q, k, v, cu_seqlens, past_len, page_table, q_rot, k
 def reatt_paged_decode(dims, q, k_pages, v_pages, page_table, seq_len, out, ws, stream=None,
                        check=True):
     """Attention of one new token per sequence over its pages."""
-    _paged_check("reatt_paged_decode", dims.dtype, (q, k_pages, v_pages, out),
-                 (page_table, seq_len), ws)
-    rc = lib.reatt_paged_decode(ctypes.byref(dims), _ptr(q), _ptr(k_pages), _ptr(v_pages),
-                                _ptr(page_table), _ptr(seq_len), _ptr(out), _ptr(ws),
+    pq, pkp, pvp, pout, ptab, plen, pws = _paged_args(
+        "reatt_paged_decode", dims.dtype, (q, k_pages, v_pages, out), (page_table, seq_len), ws)
+    rc = lib.reatt_paged_decode(ctypes.byref(dims), pq, pkp, pvp, ptab, plen, pout, pws,
                                 _stream(stream))
     if check:
         _check(rc, "reatt_paged_decode")
@@ -366,9 +364,9 @@ def reatt_paged_decode(dims, q, k_pages, v_pages, page_table, seq_len, out, ws, 
 
 def reatt_prompt_attend(dims, q, k, v, cu_seqlens, out, ws, stream=None, check=True):
     """Causal attention of whole prompts, packed."""
-    _paged_check("reatt_prompt_attend", dims.dtype, (q, k, v, out), (cu_seqlens,), ws)
-    rc = lib.reatt_prompt_attend(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens),
-                                 _ptr(out), _ptr(ws), _stream(stream))
+    pq, pk, pv, pout, pcu, pws = _paged_args("reatt_prompt_attend", dims.dtype, (q, k, v, out),
+                                             (cu_seqlens,), ws)
+    rc = lib.reatt_prompt_attend(ctypes.byref(dims), pq, pk, pv, pcu, pout, pws, _stream(stream))
     if check:
         _check(rc, "reatt_prompt_attend")
     return rc

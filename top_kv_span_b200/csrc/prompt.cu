@@ -2,12 +2,14 @@
 //
 //   o_i = sum_{t <= i} softmax_t(q_i.k_t / sqrt(d)) v_t   within each sequence
 //
-// One CTA takes 32 consecutive tokens of one query head and walks its keys 64 at
-// a time with the running maximum and sum of the softmax.  Scores and output
-// stay in registers (4 x 4 and 4 x d/16 per thread), and both products read four
-// elements of either operand at a time from shared memory.  The next K tile loads
-// during P.V and the next V tile during Q.K^T.  The arithmetic is fp32 fused
-// multiply-adds, which bound it: MEASURED.
+// One CTA takes 32 consecutive tokens of one query head.  Its groups of four warps
+// walk the keys 64 at a time in turn, each with a running maximum and sum of the
+// softmax of its own, and join at the end, so that an SM works on few blocks at a time
+// and the longest one does not outlast the others.  Scores and output stay in registers
+// (4 x 4 and 4 x d/16 per thread), and both products read four elements of either
+// operand at a time from shared memory.  A group's next K tile loads during P.V and its
+// next V tile during Q.K^T.  The arithmetic is fp32 fused multiply-adds, which bound it.
+// MEASURED
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -19,18 +21,21 @@ namespace {
 
 constexpr int kPrRows = 32;   // query tokens of a CTA
 constexpr int kPrKeys = 64;   // keys of a tile
-constexpr int kPrThreads = kPrRows / 4 * 16;
+constexpr int kPrGroup = kPrRows / 4 * 16;   // threads of a group
 
-// Padded rows: a column of them falls into different banks.
+// Padded rows: a column of them falls into different banks.  Q, then K, V and P of
+// every group, as many groups as fit.
 template <int D> struct PrSmem {
+    static constexpr int kGroups = D == 64 ? 4 : 2;
     static constexpr int RS = D + 4, PS = kPrKeys + 4;
-    static constexpr int oQ = 0, oK = oQ + kPrRows * RS, oV = oK + kPrKeys * RS,
-                         oP = oV + kPrKeys * RS;
-    static constexpr size_t kBytes = size_t(oP + kPrRows * PS) * 4;
+    static constexpr int oK = 0, oV = oK + kPrKeys * RS, oP = oV + kPrKeys * RS,
+                         kOne = oP + kPrRows * PS, oGroups = kPrRows * RS;
+    static constexpr int kThreads = kGroups * kPrGroup;
+    static constexpr size_t kBytes = size_t(oGroups + kGroups * kOne) * 4;
 };
 
 template <int D>
-__global__ void __launch_bounds__(kPrThreads)
+__global__ void __launch_bounds__(PrSmem<D>::kThreads)
 prompt_kernel(PagedGeom geo, const float *__restrict__ q, const float *__restrict__ k,
               const float *__restrict__ v, const int32_t *__restrict__ cu, float *__restrict__ out,
               float scale)
@@ -38,12 +43,14 @@ prompt_kernel(PagedGeom geo, const float *__restrict__ q, const float *__restric
     using Sm = PrSmem<D>;
     constexpr int OC = D / 16;   // output columns of a thread, in fours 64 apart
     extern __shared__ __align__(16) float sm[];
-    float *qs = sm + Sm::oQ, *ks = sm + Sm::oK, *vs = sm + Sm::oV, *ps = sm + Sm::oP;
     __shared__ PromptBlock blk_s;
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    if (tid < 32) {
+    __shared__ float2 row_ml[Sm::kGroups][kPrRows];
+    const int group = threadIdx.x / kPrGroup, tid = threadIdx.x % kPrGroup, tx = tid & 15, ty = tid >> 4;
+    float *qs = sm, *mine = sm + Sm::oGroups + group * Sm::kOne;
+    float *ks = mine + Sm::oK, *vs = mine + Sm::oV, *ps = mine + Sm::oP;
+    if (threadIdx.x < 32) {
         const PromptBlock r = prompt_block(geo, cu, kPrRows, blockIdx.x / geo.Hq);
-        if (tid == 0) blk_s = r;
+        if (threadIdx.x == 0) blk_s = r;
     }
     __syncthreads();
     const PromptBlock blk = blk_s;
@@ -51,10 +58,11 @@ prompt_kernel(PagedGeom geo, const float *__restrict__ q, const float *__restric
     const int j = blockIdx.x % geo.Hq, h = j / geo.g;
     const int nrow = min(kPrRows, blk.len - blk.q0), kend = blk.q0 + nrow;
 
+    auto meet = [&] { named_sync(1 + group, kPrGroup); };
     // `rows` rows of a packed operand from token t0 on, those past the block's last
     // token as zeros: a group of copies on its way
     auto fetch = [&](float *dst, int rows, const float *src, int64_t row_stride, int head, int t0) {
-        for (int x = tid; x < rows * (D / 4); x += kPrThreads) {
+        for (int x = tid; x < rows * (D / 4); x += kPrGroup) {
             const int r = x / (D / 4), c = (x - r * (D / 4)) * 4;
             const bool in = t0 + r < kend;
             cp_async16(smem_addr(dst + r * Sm::RS + c),
@@ -63,9 +71,15 @@ prompt_kernel(PagedGeom geo, const float *__restrict__ q, const float *__restric
         }
         cp_async_commit();
     };
-    fetch(qs, kPrRows, q, geo.qs, j, blk.q0);
-    fetch(ks, kPrKeys, k, geo.ks, h, 0);
-    fetch(vs, kPrKeys, v, geo.vs, h, 0);
+    constexpr int STEP = Sm::kGroups * kPrKeys;   // from one tile of a group to its next
+    const int first = group * kPrKeys;
+    if (group == 0) fetch(qs, kPrRows, q, geo.qs, j, blk.q0);
+    cp_async_wait<0>();
+    __syncthreads();
+    if (first < kend) {
+        fetch(ks, kPrKeys, k, geo.ks, h, first);
+        fetch(vs, kPrKeys, v, geo.vs, h, first);
+    }
 
     float o[4][OC], m[4], l[4];
 #pragma unroll
@@ -75,9 +89,9 @@ prompt_kernel(PagedGeom geo, const float *__restrict__ q, const float *__restric
 #pragma unroll
         for (int c = 0; c < OC; ++c) o[r][c] = 0.f;
     }
-    for (int k0 = 0; k0 < kend; k0 += kPrKeys) {
-        cp_async_wait<1>();   // Q and this K
-        __syncthreads();
+    for (int k0 = first; k0 < kend; k0 += STEP) {
+        cp_async_wait<1>();   // this K
+        meet();
         float s[4][4];
 #pragma unroll
         for (int r = 0; r < 4; ++r)
@@ -100,8 +114,8 @@ prompt_kernel(PagedGeom geo, const float *__restrict__ q, const float *__restric
                     s[r][c] = fmaf(a[r].w, b[c].w, s[r][c]);
                 }
         }
-        __syncthreads();
-        if (k0 + kPrKeys < kend) fetch(ks, kPrKeys, k, geo.ks, h, k0 + kPrKeys);
+        meet();
+        if (k0 + STEP < kend) fetch(ks, kPrKeys, k, geo.ks, h, k0 + STEP);
         else cp_async_commit();
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -128,7 +142,7 @@ prompt_kernel(PagedGeom geo, const float *__restrict__ q, const float *__restric
             }
         }
         cp_async_wait<1>();   // this V
-        __syncthreads();
+        meet();
         // Four keys at a time.  In the last tiles a key after the row's token takes no
         // part, whatever its value is.
         auto products = [&](bool masked) {
@@ -157,22 +171,45 @@ prompt_kernel(PagedGeom geo, const float *__restrict__ q, const float *__restric
         };
         if (k0 + kPrKeys > blk.q0) products(true);
         else products(false);
-        __syncthreads();
-        if (k0 + kPrKeys < kend) fetch(vs, kPrKeys, v, geo.vs, h, k0 + kPrKeys);
+        meet();
+        if (k0 + STEP < kend) fetch(vs, kPrKeys, v, geo.vs, h, k0 + STEP);
         else cp_async_commit();
     }
+    // join the groups: each leaves its rows' (m, l) and o (over its K tile), then every
+    // thread adds up four elements
+    meet();
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
 #pragma unroll
         for (int w = 1; w < 16; w <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], w);
-        if (ty * 4 + r < nrow) {
-            const float il = 1.f / l[r];
-            float *dst = out + (int64_t(blk.begin + blk.q0 + ty * 4 + r) * geo.Hq + j) * D;
+        if (tx == 0) row_ml[group][ty * 4 + r] = make_float2(m[r], l[r]);
 #pragma unroll
-            for (int c = 0; c < OC; c += 4)
-                *reinterpret_cast<float4 *>(dst + (c / 4) * 64 + tx * 4) =
-                    make_float4(o[r][c] * il, o[r][c + 1] * il, o[r][c + 2] * il, o[r][c + 3] * il);
+        for (int c = 0; c < OC; c += 4)
+            *reinterpret_cast<float4 *>(ks + (ty * 4 + r) * Sm::RS + (c / 4) * 64 + tx * 4) =
+                make_float4(o[r][c], o[r][c + 1], o[r][c + 2], o[r][c + 3]);
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < nrow * (D / 4); x += Sm::kThreads) {
+        const int r = x / (D / 4), c = (x - r * (D / 4)) * 4;
+        float M = row_ml[0][r].x;
+#pragma unroll
+        for (int i = 1; i < Sm::kGroups; ++i) M = fmaxf(M, row_ml[i][r].x);
+        float L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < Sm::kGroups; ++i) {
+            const float2 ml = row_ml[i][r];
+            const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+            const float4 t = *reinterpret_cast<const float4 *>(sm + Sm::oGroups + i * Sm::kOne + Sm::oK + r * Sm::RS + c);
+            L = fmaf(f, ml.y, L);
+            acc.x = fmaf(f, t.x, acc.x);
+            acc.y = fmaf(f, t.y, acc.y);
+            acc.z = fmaf(f, t.z, acc.z);
+            acc.w = fmaf(f, t.w, acc.w);
         }
+        const float il = 1.f / L;
+        *reinterpret_cast<float4 *>(out + (int64_t(blk.begin + blk.q0 + r) * geo.Hq + j) * D + c) =
+            make_float4(acc.x * il, acc.y * il, acc.z * il, acc.w * il);
     }
 }
 
@@ -187,7 +224,7 @@ cudaError_t run(const PagedGeom &g, const void *q, const void *k, const void *v,
     // every sequence has at most one block that is not full
     const int64_t blocks = (g.N / kPrRows + (g.B < g.N ? g.B : g.N)) * g.Hq;
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    kern<<<unsigned(blocks), kPrThreads, PrSmem<D>::kBytes, st>>>(
+    kern<<<unsigned(blocks), PrSmem<D>::kThreads, PrSmem<D>::kBytes, st>>>(
         g, static_cast<const float *>(q), static_cast<const float *>(k), static_cast<const float *>(v), cu,
         static_cast<float *>(out), float(1.4426950408889634 / sqrt(double(D))));
     return cudaGetLastError();

@@ -81,39 +81,45 @@ prompt_kernel(PagedGeom geo, const float *__restrict__ q, const float *__restric
         fetch(vs, kPrKeys, v, geo.vs, h, first);
     }
 
-    float o[4][OC], m[4], l[4];
+    float m[4], l[4];
+    uint64_t o[4][OC / 2];   // pairs of neighbouring columns
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         m[r] = -INFINITY;
         l[r] = 0.f;
 #pragma unroll
-        for (int c = 0; c < OC; ++c) o[r][c] = 0.f;
+        for (int c = 0; c < OC / 2; ++c) o[r][c] = 0;
     }
     for (int k0 = first; k0 < kend; k0 += STEP) {
         cp_async_wait<1>();   // this K
         meet();
+        // sums over the even and the odd elements of d side by side
+        uint64_t s2[4][4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s2[r][c] = 0;
+#pragma unroll 4
+        for (int e = 0; e < D; e += 4) {
+            ulonglong2 a[4], b[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) a[r] = *reinterpret_cast<const ulonglong2 *>(qs + (ty * 4 + r) * Sm::RS + e);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) b[c] = *reinterpret_cast<const ulonglong2 *>(ks + (tx + 16 * c) * Sm::RS + e);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) s2[r][c] = fma2(a[r].y, b[c].y, fma2(a[r].x, b[c].x, s2[r][c]));
+        }
         float s[4][4];
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) s[r][c] = 0.f;
-#pragma unroll 4
-        for (int e = 0; e < D; e += 4) {
-            float4 a[4], b[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) a[r] = *reinterpret_cast<const float4 *>(qs + (ty * 4 + r) * Sm::RS + e);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) b[c] = *reinterpret_cast<const float4 *>(ks + (tx + 16 * c) * Sm::RS + e);
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    s[r][c] = fmaf(a[r].x, b[c].x, s[r][c]);
-                    s[r][c] = fmaf(a[r].y, b[c].y, s[r][c]);
-                    s[r][c] = fmaf(a[r].z, b[c].z, s[r][c]);
-                    s[r][c] = fmaf(a[r].w, b[c].w, s[r][c]);
-                }
-        }
+            for (int c = 0; c < 4; ++c) {
+                float even, odd;
+                unpack2(s2[r][c], even, odd);
+                s[r][c] = even + odd;
+            }
         meet();
         if (k0 + STEP < kend) fetch(ks, kPrKeys, k, geo.ks, h, k0 + STEP);
         else cp_async_commit();
@@ -132,8 +138,9 @@ prompt_kernel(PagedGeom geo, const float *__restrict__ q, const float *__restric
             const float fac = m[r] == -INFINITY ? 0.f : ex2_approx(m[r] - mn);
             m[r] = mn;
             l[r] *= fac;
+            const uint64_t fac2 = pack2(fac, fac);
 #pragma unroll
-            for (int c = 0; c < OC; ++c) o[r][c] *= fac;
+            for (int c = 0; c < OC / 2; ++c) o[r][c] = mul2(o[r][c], fac2);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const float p = s[r][c] == -INFINITY ? 0.f : ex2_approx(s[r][c] - mn);
@@ -153,18 +160,20 @@ prompt_kernel(PagedGeom geo, const float *__restrict__ q, const float *__restric
                 for (int r = 0; r < 4; ++r) p[r] = *reinterpret_cast<const float4 *>(ps + (ty * 4 + r) * Sm::PS + kk);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float vv[OC];
+                    uint64_t vv[OC / 2];
 #pragma unroll
                     for (int c = 0; c < OC; c += 4) {
-                        const float4 t = *reinterpret_cast<const float4 *>(vs + (kk + i) * Sm::RS + (c / 4) * 64 + tx * 4);
-                        vv[c] = t.x; vv[c + 1] = t.y; vv[c + 2] = t.z; vv[c + 3] = t.w;
+                        const ulonglong2 t = *reinterpret_cast<const ulonglong2 *>(vs + (kk + i) * Sm::RS + (c / 4) * 64 + tx * 4);
+                        vv[c / 2] = t.x;
+                        vv[c / 2 + 1] = t.y;
                     }
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         if (masked && k0 + kk + i > blk.q0 + ty * 4 + r) continue;
                         const float w = i == 0 ? p[r].x : i == 1 ? p[r].y : i == 2 ? p[r].z : p[r].w;
+                        const uint64_t w2 = pack2(w, w);
 #pragma unroll
-                        for (int c = 0; c < OC; ++c) o[r][c] = fmaf(w, vv[c], o[r][c]);
+                        for (int c = 0; c < OC / 2; ++c) o[r][c] = fma2(w2, vv[c], o[r][c]);
                     }
                 }
             }
@@ -185,8 +194,8 @@ prompt_kernel(PagedGeom geo, const float *__restrict__ q, const float *__restric
         if (tx == 0) row_ml[group][ty * 4 + r] = make_float2(m[r], l[r]);
 #pragma unroll
         for (int c = 0; c < OC; c += 4)
-            *reinterpret_cast<float4 *>(ks + (ty * 4 + r) * Sm::RS + (c / 4) * 64 + tx * 4) =
-                make_float4(o[r][c], o[r][c + 1], o[r][c + 2], o[r][c + 3]);
+            *reinterpret_cast<ulonglong2 *>(ks + (ty * 4 + r) * Sm::RS + (c / 4) * 64 + tx * 4) =
+                make_ulonglong2(o[r][c / 2], o[r][c / 2 + 1]);
     }
     __syncthreads();
     for (int x = threadIdx.x; x < nrow * (D / 4); x += Sm::kThreads) {

@@ -567,7 +567,7 @@ paged_decode_bf16_kernel(PagedGeom geo, PdArgs a)
 
 // The join: block i finishes the unit that begins in range i and goes on in the
 // following ranges.  Every partial's weight is formed once; then groups of threads
-// take every kJoinGroups-th partial, four elements a thread with several loads in
+// take every so many-th partial, four elements a thread with several loads in
 // flight, and the groups' sums are added in order.
 constexpr int kJoinThreads = 512, kJoinParts = 64;
 template <typename T, int D, int HB>

@@ -335,8 +335,10 @@ REATT_API int reatt_merge_partials(const reatt_dims *dims, int32_t n_parts,
  *
  * A page id outside [0, n_pages), or a length outside [0, max_pages * page],
  * never leads out of the pools: such tokens are left out (lengths are clamped)
- * and REATT_EPAGE is recorded in the workspace status word; the results of that
- * sequence are then unspecified.
+ * and REATT_EPAGE is recorded in the workspace status word (which keeps the larger
+ * of several codes until it is read); the results of that sequence are then
+ * unspecified.  Offsets that are not ascending or pass N give unspecified results
+ * for the packed rows, but every access stays inside them.
  * --------------------------------------------------------------------------- */
 typedef struct {
     int32_t B;            /* sequences                          1 <= B <= 65536     */

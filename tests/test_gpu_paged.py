@@ -707,3 +707,15 @@ def test_prompt_captured_with_lengths_that_change(R):
                 at += n
             assert (out[at:] == 5.0).all()
         assert R.reatt_workspace_status(ws) == R.OK
+
+
+def test_thousands_of_sequences(R):
+    """More sequences than any table in a kernel keeps at hand, most of them empty."""
+    B = 9000
+    lens = [0] * B
+    for b, n in ((0, 3), (17, 70), (4095, 1), (4096, 200), (8191, 64), (8998, 33), (8999, 5)):
+        lens[b] = n
+    run_decode(R, 4, 1, 64, BF16, 16, lens)
+    for dtype in (BF16, F32):
+        run_prompt(R, 4, 1, 64, dtype, lens, before=2, after=2)
+    run_append(R, 4, 1, 64, BF16, 16, [0] * B, lens, 1e4, before=1, after=2)

@@ -144,3 +144,19 @@ def test_host_tensors_are_refused(R):
         R.reatt_prompt_attend(d, A, A, A, torch.zeros(4, dtype=torch.int32), A, A, stream=0)
     with pytest.raises(R.ReattError):
         append(R, d, ws=torch.zeros(1 << 20, dtype=torch.uint8))
+
+
+def test_more_prompt_blocks_than_a_grid(R):
+    # one token a block and thousands of heads: refused before any CUDA call
+    d = dims(R, Hq=4096, Hkv=32, d=64, N=(1 << 28) - 1)
+    assert prompt(R, d) == R.EUNSUPPORTED
+    d = dims(R, Hq=4096, Hkv=4096, d=64, N=(1 << 28) - 1, dtype="f32")
+    assert prompt(R, d) == R.EUNSUPPORTED
+
+
+def test_unknown_dtypes_are_refused(R):
+    for dtype in ("fp16", torch.float16, torch.float64):
+        with pytest.raises(R.ReattError) as e:
+            dims(R, dtype=dtype)
+        assert e.value.code == R.EUNSUPPORTED
+    assert dims(R, dtype=torch.float32).dtype == R.F32 and dims(R, dtype="bf16").dtype == R.BF16

@@ -140,8 +140,10 @@ int reatt_prompt_attend(const reatt_paged_dims *dims, const void *q, const void 
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(cu_seqlens) || !aligned16(out) ||
         !aligned16(ws))
         return REATT_EINVAL;
-    return cuda_status(launch_prompt(g, q, k, v, cu_seqlens, out, ws,
-                                     reinterpret_cast<cudaStream_t>(stream)));
+    const cudaError_t e = launch_prompt(g, q, k, v, cu_seqlens, out, ws,
+                                        reinterpret_cast<cudaStream_t>(stream));
+    // more blocks than a grid holds (rows of one token each, thousands of heads)
+    return e == cudaErrorInvalidConfiguration ? REATT_EUNSUPPORTED : cuda_status(e);
 }
 
 }  // extern "C"

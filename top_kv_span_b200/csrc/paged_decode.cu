@@ -146,12 +146,13 @@ template <typename T, int D, bool SWIZZLE> struct PdStream {
 template <typename T, int D>
 __device__ __forceinline__ void pd_empty(const PagedGeom &geo, const PdArgs &a)
 {
-    for (int b = blockIdx.x; b < geo.B; b += gridDim.x) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;   // a warp per sequence
+    for (int b = blockIdx.x * kPdWarps + warp; b < geo.B; b += gridDim.x * kPdWarps) {
         const int len = pd_len(geo, a.lens, b);
         if (len == 0)
-            for (int i = threadIdx.x; i < geo.Hq * D; i += kPdThreads)
+            for (int i = lane; i < geo.Hq * D; i += 32)
                 store_elem(static_cast<T *>(a.out) + int64_t(b) * geo.Hq * D + i, 0.f);
-        if (threadIdx.x == 0 && len != a.lens[b]) report_status(a.ws, REATT_EPAGE);
+        if (lane == 0 && len != a.lens[b]) report_status(a.ws, REATT_EPAGE);
     }
 }
 

@@ -229,13 +229,12 @@ template <int D>
 cudaError_t run(const PagedGeom &g, const void *q, const void *k, const void *v, const int32_t *cu,
                 void *out, cudaStream_t st)
 {
+    const int64_t blocks = prompt_blocks(g, kPrRows) * g.Hq;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
     auto kern = prompt_kernel<D>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          int(PrSmem<D>::kBytes));
     if (e != cudaSuccess) return e;
-    // every sequence has at most one block that is not full
-    const int64_t blocks = (g.N / kPrRows + (g.B < g.N ? g.B : g.N)) * g.Hq;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
     kern<<<unsigned(blocks), PrSmem<D>::kThreads, PrSmem<D>::kBytes, st>>>(
         g, static_cast<const float *>(q), static_cast<const float *>(k), static_cast<const float *>(v), cu,
         static_cast<float *>(out), float(1.4426950408889634 / sqrt(double(D))));

@@ -5,6 +5,9 @@
 
 namespace reatt {
 
+// Blocks of TB tokens at most: every sequence has at most one that is not full.
+inline int64_t prompt_blocks(const PagedGeom &g, int TB) { return g.N / TB + (g.B < g.N ? g.B : g.N); }
+
 struct PromptBlock {
     int begin, len;   // the sequence's first packed row and its length
     int q0;           // the block's first token within the sequence

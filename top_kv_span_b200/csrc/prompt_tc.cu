@@ -47,6 +47,7 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "kernels.h"
@@ -213,9 +214,10 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     auto wait = [&](uint64_t *bar, int use) {
         return mbar_wait_bounded(bar, uint32_t(use) & 1u, kWaitLimitNs);
     };
-    // the same by polling, for the waits of the chain S -> P -> O: a poll answers sooner than a suspended wait, and reading the
-    // global timer would take longer than most waits, so the limit counts polls
-    // (2^26 of at least 20 cycles); it also ends when another wait has failed
+    // the same by polling, for the waits of the chain S -> P -> O: a poll answers sooner
+    // than a suspended wait, and reading the global timer would take longer than most
+    // waits, so the limit counts polls (2^26 of at least 20 cycles); it also ends when
+    // another wait has failed
     auto poll = [&](uint64_t *bar, int use) {
         for (int i = 1; !mbar_test(bar, uint32_t(use) & 1u); ++i)
             if ((i & 1023) == 0 && (aborted() || i >= (1 << 26))) return false;
@@ -482,7 +484,10 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                     }
                     fence_proxy_async_smem();   // before this warp's arrival for P(j)
                 }
-                if (!__all_sync(0xffffffffu, poll(&sh.sfull[t][g & 1], g >> 1))) return false;
+                // (one vote at the step's end asks whether the polls succeeded: until then
+                // a failed one only means values that go nowhere)
+                bool fine = poll(&sh.sfull[t][g & 1], g >> 1);
+                __syncwarp();
                 tc_fence_after();
                 float s[kPtKeys];
                 {
@@ -538,7 +543,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 }
                 // masked keys are -inf and give 0; without any key yet m is -inf: all give 0
                 const float mc = m == -INFINITY ? 0.f : m * scale;
-                if (!__all_sync(0xffffffffu, my_turn(j))) return false;
+                fine = my_turn(j) && fine;
+                __syncwarp();
                 const uint64_t sc2 = pack2(scale, scale), mc2 = pack2(-mc, -mc);
                 uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -560,7 +566,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                __syncwarp();
+                if (!__all_sync(0xffffffffu, fine)) return false;
                 if (lane == 0) mbar_arrive(&sh.pfull[t][g & 1]);
                 const uint64_t l2 = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
                 float l0, l1;
@@ -658,15 +664,17 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
 bool packed_map(CUtensorMap *mp, const void *base, int64_t N, int H, int d, int64_t row_stride,
                 uint32_t heads, uint32_t tokens)
 {
-    // the driver's encoder, looked up once (a magic static: thread-safe)
-    static const PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
+    // the driver's encoder, looked up until it is found
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> found{nullptr};
+    PFN_cuTensorMapEncodeTiled_v12000 enc = found.load(std::memory_order_relaxed);
+    if (!enc) {
         void *p = nullptr;
         cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }();
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+        found.store(enc, std::memory_order_relaxed);
+    }
     if (!enc) return false;
     cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(H), cuuint64_t(N)};
     cuuint64_t strides[2] = {cuuint64_t(d) * 2, cuuint64_t(row_stride) * 2};
@@ -682,14 +690,13 @@ cudaError_t run(const PagedGeom &g, const void *q, const void *k, const void *v,
                 void *out, void *ws, cudaStream_t st)
 {
     const int TPT = kPtRows / g.g, TB = 2 * TPT;
+    const int64_t blocks = prompt_blocks(g, TB) * g.Hkv;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
     CUtensorMap qm, km, vm;
     if (!packed_map(&qm, q, g.N, g.Hq, D, g.qs, uint32_t(g.g), uint32_t(TPT)) ||
         !packed_map(&km, k, g.N, g.Hkv, D, g.ks, 1, kPtKeys) ||
         !packed_map(&vm, v, g.N, g.Hkv, D, g.vs, 1, kPtKeys))
         return cudaErrorInvalidValue;
-    // every sequence has at most one block that is not full
-    const int64_t blocks = (g.N / TB + (g.B < g.N ? g.B : g.N)) * g.Hkv;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
     auto kern = prompt_tc_kernel<D>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          int(PtSmem<D>::kBytes));

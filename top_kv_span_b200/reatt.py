@@ -299,11 +299,13 @@ def reatt_merge_partials(dims, n_parts, part_ml_all, part_acc_all, out, stream=N
 def make_paged_dims(B, Hq, Hkv, d, dtype, N, page=1, max_pages=1, n_pages=1, rope_base=0.0,
                     q_stride=0, k_stride=0, v_stride=0, q_rot_stride=0,
                     k_rot_stride=0) -> reatt_paged_dims:
-    """Dims of the paged calls (strides in elements between packed rows, 0 = dense)."""
-    if isinstance(dtype, str):
-        dtype = F32 if dtype == "f32" else BF16
-    elif isinstance(dtype, torch.dtype):
-        dtype = F32 if dtype == torch.float32 else BF16
+    """Dims of the paged calls (strides in elements between packed rows, 0 = dense).
+    dtype: "f32", "bf16", the torch dtypes of these, or a reatt_dtype code."""
+    codes = {"f32": F32, "bf16": BF16, torch.float32: F32, torch.bfloat16: BF16}
+    if not isinstance(dtype, int):
+        if dtype not in codes:
+            raise ReattError(EUNSUPPORTED, f"make_paged_dims: dtype {dtype}")
+        dtype = codes[dtype]
     return reatt_paged_dims(int(B), int(Hq), int(Hkv), int(d), int(dtype), int(page),
                             int(max_pages), 0, int(N), int(n_pages), int(q_stride), int(k_stride),
                             int(v_stride), int(q_rot_stride), int(k_rot_stride), float(rope_base))

@@ -68,6 +68,7 @@ paged_append_kernel(PagedGeom geo, AppendArgs a)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t t0 = int64_t(blockIdx.x) * a.tokens;
 
+    pdl_wait();
     if (a.seq_len)
         for (int64_t b = int64_t(blockIdx.x) * blockDim.x + tid; b < geo.B;
              b += int64_t(gridDim.x) * blockDim.x) {
@@ -174,8 +175,7 @@ cudaError_t launch_paged_append(const PagedGeom &g, const void *q, const void *k
     auto kern = g.dtype == REATT_BF16
                     ? (g.d == 128 ? paged_append_kernel<uint16_t, 128> : paged_append_kernel<uint16_t, 64>)
                     : (g.d == 128 ? paged_append_kernel<float, 128> : paged_append_kernel<float, 64>);
-    kern<<<unsigned(blocks), kAppThreads, 0, st>>>(g, a);
-    return cudaGetLastError();
+    return launch_pdl(kern, dim3(unsigned(blocks)), dim3(kAppThreads), 0, st, g, a);
 }
 
 }  // namespace reatt

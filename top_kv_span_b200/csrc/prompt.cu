@@ -51,6 +51,7 @@ prompt_kernel(PagedGeom geo, const float *__restrict__ q, const float *__restric
     const int group = threadIdx.x / kPrGroup, tid = threadIdx.x % kPrGroup, tx = tid & 15, ty = tid >> 4;
     float *qs = sm, *mine = sm + Sm::oGroups + group * Sm::kOne;
     float *ks = mine + Sm::oK, *vs = mine + Sm::oV, *ps = mine + Sm::oP;
+    pdl_wait();
     if (threadIdx.x < 32) {
         const PromptBlock r = prompt_block(geo, cu, kPrRows, blockIdx.x / geo.Hq);
         if (threadIdx.x == 0) blk_s = r;
@@ -235,10 +236,10 @@ cudaError_t run(const PagedGeom &g, const void *q, const void *k, const void *v,
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          int(PrSmem<D>::kBytes));
     if (e != cudaSuccess) return e;
-    kern<<<unsigned(blocks), PrSmem<D>::kThreads, PrSmem<D>::kBytes, st>>>(
-        g, static_cast<const float *>(q), static_cast<const float *>(k), static_cast<const float *>(v), cu,
-        static_cast<float *>(out), float(1.4426950408889634 / sqrt(double(D))));
-    return cudaGetLastError();
+    return launch_pdl(kern, dim3(unsigned(blocks)), dim3(PrSmem<D>::kThreads), PrSmem<D>::kBytes, st, g,
+                      static_cast<const float *>(q), static_cast<const float *>(k),
+                      static_cast<const float *>(v), cu, static_cast<float *>(out),
+                      float(1.4426950408889634 / sqrt(double(D))));
 }
 
 }  // namespace

@@ -201,6 +201,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         }
         mbar_init_fence();
     }
+    pdl_wait();   // the set-up above may run beside the end of the kernel before
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -701,10 +702,9 @@ cudaError_t run(const PagedGeom &g, const void *q, const void *k, const void *v,
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          int(PtSmem<D>::kBytes));
     if (e != cudaSuccess) return e;
-    kern<<<unsigned(blocks), kPtThreads, PtSmem<D>::kBytes, st>>>(
-        qm, km, vm, g, cu, static_cast<const uint16_t *>(v), static_cast<uint16_t *>(out),
-        float(1.4426950408889634 / sqrt(double(D))), ws);
-    return cudaGetLastError();
+    return launch_pdl(kern, dim3(unsigned(blocks)), dim3(kPtThreads), PtSmem<D>::kBytes, st, qm, km, vm, g,
+                      cu, static_cast<const uint16_t *>(v), static_cast<uint16_t *>(out),
+                      float(1.4426950408889634 / sqrt(double(D))), ws);
 }
 
 }  // namespace

@@ -575,12 +575,10 @@ template <typename T, int D, int HB>
 __global__ void __launch_bounds__(kJoinThreads)
 paged_decode_join_kernel(PagedGeom geo, PdArgs a)
 {
-    constexpr int WORDS = HB * D / 4;                  // float4 words of a partial
-    constexpr int GROUPS = WORDS >= kJoinThreads ? 1 : kJoinThreads / WORDS;
-    constexpr int PER = WORDS <= kJoinThreads ? 1 : WORDS / kJoinThreads;
+    static_assert(HB * D / 4 <= kJoinThreads, "a thread takes at most one word");
     __shared__ int last_s;
     __shared__ float top[HB], total[HB], weight[kJoinParts][HB];
-    __shared__ float4 sums[GROUPS > 1 ? GROUPS : 1][GROUPS > 1 ? WORDS : 1];
+    __shared__ float4 sums[kJoinThreads];
     const int tid = threadIdx.x, n = gridDim.x, first = blockIdx.x;
     if (tid == 0) last_s = n - 1;
     pdl_wait();
@@ -617,61 +615,47 @@ paged_decode_join_kernel(PagedGeom geo, PdArgs a)
             total[j] = L;
         }
     }
-    float4 acc[PER];
-#pragma unroll
-    for (int r = 0; r < PER; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int group = PER > 1 ? 0 : tid / WORDS;
+    // groups of threads, one float4 word of the heads a thread
+    const int words = nh * D / 4, groups = kJoinThreads / words, group = tid / words, word = tid % words;
+    const int j = word * 4 / D;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int x0 = 0; x0 < parts; x0 += kJoinParts) {
         const int np = min(kJoinParts, parts - x0);
         __syncthreads();
-        for (int y = tid; y < np * HB; y += kJoinThreads) {
-            const int x = y / HB, j = y - x * HB;
-            weight[x][j] = j < nh ? pd_weight(a.part_ml[slot_of(x0 + x) * HB + j].x, top[j]) : 0.f;
+        for (int y = tid; y < np * nh; y += kJoinThreads) {
+            const int x = y / nh, i = y - x * nh;
+            weight[x][i] = pd_weight(a.part_ml[slot_of(x0 + x) * HB + i].x, top[i]);
         }
         __syncthreads();
-#pragma unroll
-        for (int r = 0; r < PER; ++r) {
-            const int word = PER > 1 ? r * kJoinThreads + tid : tid % WORDS, j = word * 4 / D;
-            if (j < nh && group < GROUPS) {
+        if (group < groups)
 #pragma unroll 8
-                for (int x = group; x < np; x += GROUPS) {
-                    const float4 v = reinterpret_cast<const float4 *>(
-                        a.part_acc + int64_t(slot_of(x0 + x)) * HB * D)[word];
-                    const float f = weight[x][j];
-                    acc[r].x = fmaf(f, v.x, acc[r].x);
-                    acc[r].y = fmaf(f, v.y, acc[r].y);
-                    acc[r].z = fmaf(f, v.z, acc[r].z);
-                    acc[r].w = fmaf(f, v.w, acc[r].w);
-                }
+            for (int x = group; x < np; x += groups) {
+                const float4 v =
+                    reinterpret_cast<const float4 *>(a.part_acc + int64_t(slot_of(x0 + x)) * HB * D)[word];
+                const float f = weight[x][j];
+                acc.x = fmaf(f, v.x, acc.x);
+                acc.y = fmaf(f, v.y, acc.y);
+                acc.z = fmaf(f, v.z, acc.z);
+                acc.w = fmaf(f, v.w, acc.w);
             }
-        }
     }
-    if constexpr (GROUPS > 1) {
-        sums[group][tid % WORDS] = acc[0];
-        __syncthreads();
-        if (group > 0) return;
-#pragma unroll
-        for (int i = 1; i < GROUPS; ++i) {
-            const float4 v = sums[i][tid];
-            acc[0].x += v.x;
-            acc[0].y += v.y;
-            acc[0].z += v.z;
-            acc[0].w += v.w;
-        }
+    sums[tid] = acc;
+    __syncthreads();
+    if (group > 0) return;
+    for (int i = 1; i < groups; ++i) {
+        const float4 v = sums[i * words + tid];
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
     }
-#pragma unroll
-    for (int r = 0; r < PER; ++r) {
-        const int word = PER > 1 ? r * kJoinThreads + tid : tid % WORDS;
-        const int j = word * 4 / D, c = word * 4 - j * D;
-        if (j < nh) {
-            T *dst = static_cast<T *>(a.out) + (int64_t(me.open_b) * geo.Hq + h * geo.g + j0 + j) * D + c;
-            const float il = 1.f / total[j];
-            store_elem(dst, acc[r].x * il);
-            store_elem(dst + 1, acc[r].y * il);
-            store_elem(dst + 2, acc[r].z * il);
-            store_elem(dst + 3, acc[r].w * il);
-        }
-    }
+    const int c = word * 4 - j * D;
+    T *dst = static_cast<T *>(a.out) + (int64_t(me.open_b) * geo.Hq + h * geo.g + j0 + j) * D + c;
+    const float il = 1.f / total[j];
+    store_elem(dst, acc.x * il);
+    store_elem(dst + 1, acc.y * il);
+    store_elem(dst + 2, acc.z * il);
+    store_elem(dst + 3, acc.w * il);
 }
 
 constexpr int kPdResident = 2;   // CTAs of an SM, at most

@@ -31,6 +31,14 @@ template <> __device__ __forceinline__ void store_elem<uint16_t>(uint16_t *p, fl
     *reinterpret_cast<__nv_bfloat16 *>(p) = __float2bfloat16_rn(v);
 }
 
+__device__ __forceinline__ void store4(float *p, const float4 &v) { *reinterpret_cast<float4 *>(p) = v; }
+__device__ __forceinline__ void store4(uint16_t *p, const float4 &v)
+{
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&a),
+                                               *reinterpret_cast<const uint32_t *>(&b));
+}
+
 // E consecutive elements of a row, widened.
 template <int E> __device__ __forceinline__ void load_slice(const float *p, float (&v)[E])
 {
@@ -98,12 +106,14 @@ template <typename T, int D, bool SWIZZLE> struct PdStream {
     // Issue the next tile's copies (none past the end); one group either way.
     __device__ __forceinline__ void load()
     {
+        const int lane = threadIdx.x & 31, key = at.tile * TILE + key_of_lane;
         if (left > 0) {
-            const int lane = threadIdx.x & 31, key = at.tile * TILE + key_of_lane;
             const uint32_t st = ring + uint32_t(slot) * kPdStage;
             const uint8_t *kp = static_cast<const uint8_t *>(a.k_pages);
             const uint8_t *vp = static_cast<const uint8_t *>(a.v_pages);
-            if (one_page && key - lane + KT <= at.len && uint32_t(__shfl_sync(0xffffffffu, id, 0)) < geo.n_pages) {
+            if (key - lane >= at.len) {
+                // no key of this warp's: the part is passed over
+            } else if (one_page && key - lane + KT <= at.len && uint32_t(__shfl_sync(0xffffffffu, id, 0)) < geo.n_pages) {
                 // all rows there and contiguous: every lane's words lie 512 bytes apart
                 const int64_t first = key_row(geo, __shfl_sync(0xffffffffu, id, 0), at.u / a.chunks,
                                               key - lane, D) * int64_t(sizeof(T)) + lane * 16;
@@ -156,6 +166,10 @@ __device__ __forceinline__ void pd_empty(const PagedGeom &geo, const PdArgs &a)
     }
 }
 
+// Rows of the warps' o are padded by four floats: the lanes of a product's columns then
+// write to different banks.
+constexpr int kPdPad = 4;
+
 // Joins the warps' (m, l, o) of a unit's part, which they have left in red_ml and
 // red_o, and finishes the unit or leaves the part for the join kernel.  Every thread
 // of the CTA calls it after a barrier, and passes another one before it writes there
@@ -168,23 +182,30 @@ __device__ __forceinline__ void pd_finish(const PagedGeom &geo, const PdArgs &a,
     const int h = w.u / a.chunks, j0 = (w.u % a.chunks) * HB, nh = min(HB, geo.g - j0);
     const bool whole = begins && ends;
     const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
-    for (int y = threadIdx.x; y < nh * D; y += kPdThreads) {
-        const int j = y / D, c = y - j * D;
+    for (int y = threadIdx.x; y < nh * (D / 4); y += kPdThreads) {
+        const int j = y / (D / 4), c = (y - j * (D / 4)) * 4;
         float M = red_ml[0][j].x;
 #pragma unroll
         for (int i = 1; i < kPdWarps; ++i) M = fmaxf(M, red_ml[i][j].x);
-        float L = 0.f, acc = 0.f;
+        float L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < kPdWarps; ++i) {
-            const float f = pd_weight(red_ml[i][j].x, M);
-            L += f * red_ml[i][j].y;
-            acc += f * red_o[(i * HB + j) * D + c];
+            const float2 ml = red_ml[i][j];
+            if (ml.y == 0.f) continue;   // no key, or no weight: its o was not left
+            const float f = pd_weight(ml.x, M);
+            const float4 t = *reinterpret_cast<const float4 *>(red_o + (i * HB + j) * (D + kPdPad) + c);
+            L = fmaf(f, ml.y, L);
+            acc.x = fmaf(f, t.x, acc.x);
+            acc.y = fmaf(f, t.y, acc.y);
+            acc.z = fmaf(f, t.z, acc.z);
+            acc.w = fmaf(f, t.w, acc.w);
         }
         if (whole) {
-            store_elem(static_cast<T *>(a.out) + (int64_t(w.b) * geo.Hq + h * geo.g + j0 + j) * D + c,
-                       acc / L);
+            store4(static_cast<T *>(a.out) + (int64_t(w.b) * geo.Hq + h * geo.g + j0 + j) * D + c,
+                   make_float4(acc.x / L, acc.y / L, acc.z / L, acc.w / L));
         } else {
-            a.part_acc[(int64_t(slot) * HB + j) * D + c] = acc;
+            store4(a.part_acc + (int64_t(slot) * HB + j) * D + c, acc);
             if (c == 0) a.part_ml[slot * HB + j] = make_float2(M, L);
         }
     }
@@ -229,36 +250,42 @@ paged_decode_f32_kernel(PagedGeom geo, PdArgs a)
 #pragma unroll
     for (int s = 0; s < kPdStages - 1; ++s) stream.load();
 
-    float qv[HB][E], o[HB][E], m = -INFINITY, l = 0.f;   // m, l: of head lane % HB
-    bool fresh = true;
+    float qv[HB][E], o[HB][E], m, l;   // m, l: of head lane % HB
+    auto load_q = [&](const PdWalk &w) {
+        const int h = w.u / a.chunks, j0 = (w.u % a.chunks) * HB, nh = min(HB, geo.g - j0);
+#pragma unroll
+        for (int j = 0; j < HB; ++j) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) qv[j][e] = 0.f;
+            if (j < nh)
+                load_slice<E>(static_cast<const float *>(a.q) + int64_t(w.b) * geo.qs +
+                                  int64_t(h * geo.g + j0 + j) * D + lane * E,
+                              qv[j]);
+        }
+    };
+    auto reset = [&] {
+#pragma unroll
+        for (int j = 0; j < HB; ++j)
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[j][e] = 0.f;
+        m = -INFINITY;
+        l = 0.f;
+    };
+    load_q(cw);
+    reset();
     bool begins = cw.tile == 0;   // this part of the unit starts at its first key
     int slot = 0;
     for (int64_t i = 0; i < n; ++i) {
-        const int h = cw.u / a.chunks, j0 = (cw.u % a.chunks) * HB;   // first query head of the unit
-        const int nh = min(HB, geo.g - j0);
-        if (fresh) {
-#pragma unroll
-            for (int j = 0; j < HB; ++j) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) qv[j][e] = o[j][e] = 0.f;
-                if (j < nh)
-                    load_slice<E>(static_cast<const float *>(a.q) + int64_t(cw.b) * geo.qs +
-                                      int64_t(h * geo.g + j0 + j) * D + lane * E,
-                                  qv[j]);
-            }
-            m = -INFINITY;
-            l = 0.f;
-            fresh = false;
-        }
         stream.load();
         cp_async_wait<kPdStages - 1>();
         __syncwarp();
         const float *kt = reinterpret_cast<const float *>(ring + slot * kPdStage);
         const float *vt = kt + kPdHalf / 4;
         const int key0 = cw.tile * TILE + warp * KT;
+        const bool has = key0 < cw.len;   // some key of the tile is this warp's
         float x[NB];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
+        for (int nb = 0; has && nb < NB; ++nb) {
             constexpr int KPB = 32 / HB;   // keys of one butterfly
             float v[32];
 #pragma unroll
@@ -283,42 +310,50 @@ paged_decode_f32_kernel(PagedGeom geo, PdArgs a)
                 }
             x[nb] = key0 + nb * KPB + lane / HB < cw.len ? v[0] * a.scale : -INFINITY;
         }
-        float mx = x[0];
-#pragma unroll
-        for (int nb = 1; nb < NB; ++nb) mx = fmaxf(mx, x[nb]);
-#pragma unroll
-        for (int w = HB; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-        const float mn = fmaxf(m, mx), fac = pd_weight(m, mn);
-        m = mn;
-        float p[NB], ps = 0.f;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            // a masked key is -inf; a row of logits that are all -inf keeps l = 0
-            p[nb] = x[nb] == -INFINITY ? 0.f : ex2_approx(x[nb] - m);
-            ps += p[nb];
+        // the last product with this unit's q: the next one's is on its way meanwhile
+        const bool unit_end = cw.tile + 1 == cw.nt, part_end = unit_end || i + 1 == n;
+        PdWalk nw = cw;
+        if (i + 1 < n) {
+            nw.next<TILE>(geo, a.lens, units);
+            if (part_end) load_q(nw);
         }
-        l = l * fac + ps;
+        if (has) {
+            float mx = x[0];
 #pragma unroll
-        for (int j = 0; j < HB; ++j) {
-            const float f = __shfl_sync(0xffffffffu, fac, j);
+            for (int nb = 1; nb < NB; ++nb) mx = fmaxf(mx, x[nb]);
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[j][e] *= f;
-        }
+            for (int w = HB; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+            const float mn = fmaxf(m, mx), fac = pd_weight(m, mn);
+            m = mn;
+            float p[NB], ps = 0.f;
 #pragma unroll
-        for (int kk = 0; kk < KT; ++kk) {
-            float vv[E];
-            load_slice<E>(vt + kk * D + lane * E, vv);
+            for (int nb = 0; nb < NB; ++nb) {
+                // a masked key is -inf; a row of logits that are all -inf keeps l = 0
+                p[nb] = x[nb] == -INFINITY ? 0.f : ex2_approx(x[nb] - m);
+                ps += p[nb];
+            }
+            l = l * fac + ps;
 #pragma unroll
             for (int j = 0; j < HB; ++j) {
-                const float pj = __shfl_sync(0xffffffffu, p[kk * HB / 32], (kk * HB) % 32 + j);
+                const float f = __shfl_sync(0xffffffffu, fac, j);
 #pragma unroll
-                for (int e = 0; e < E; ++e) o[j][e] = fmaf(pj, vv[e], o[j][e]);
+                for (int e = 0; e < E; ++e) o[j][e] *= f;
+            }
+#pragma unroll
+            for (int kk = 0; kk < KT; ++kk) {
+                float vv[E];
+                load_slice<E>(vt + kk * D + lane * E, vv);
+#pragma unroll
+                for (int j = 0; j < HB; ++j) {
+                    const float pj = __shfl_sync(0xffffffffu, p[kk * HB / 32], (kk * HB) % 32 + j);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) o[j][e] = fmaf(pj, vv[e], o[j][e]);
+                }
             }
         }
         __syncwarp();   // the stage may be refilled
         slot = slot + 1 == kPdStages ? 0 : slot + 1;
-        const bool unit_end = cw.tile + 1 == cw.nt;
-        if (unit_end || i + 1 == n) {
+        if (part_end) {
             // join the warps, then finish the unit or leave it for the join kernel
 #pragma unroll
             for (int w = HB; w < 32; w <<= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
@@ -327,12 +362,15 @@ paged_decode_f32_kernel(PagedGeom geo, PdArgs a)
 #pragma unroll
             for (int j = 0; j < HB; ++j)
 #pragma unroll
-                for (int e = 0; e < E; ++e) red_o[(warp * HB + j) * D + lane * E + e] = o[j][e];
+                for (int e = 0; e < E; e += 2)
+                    *reinterpret_cast<float2 *>(red_o + (warp * HB + j) * (D + kPdPad) + lane * E + e) =
+                        make_float2(o[j][e], o[j][e + 1]);
             __syncthreads();
             pd_finish<float, D, HB>(geo, a, cw, begins, unit_end, red_ml, red_o);
-            fresh = begins = true;
+            begins = true;
+            reset();
         }
-        if (i + 1 < n) cw.next<TILE>(geo, a.lens, units);
+        cw = nw;
     }
     cp_async_wait<0>();
 }
@@ -442,26 +480,29 @@ paged_decode_bf16_kernel(PagedGeom geo, PdArgs a)
         __syncwarp();
         const uint32_t kt = ring + uint32_t(slot) * kPdStage, vt = kt + kPdHalf;
         const int key0 = cw.tile * TILE + warp * KT;
+        const bool has = key0 < cw.len;   // some key of the tile is this warp's
         float x[KG][HT][4];
+        if (has) {
 #pragma unroll
-        for (int kg = 0; kg < KG; ++kg) {
-            // two chains of products each, added at the end
-            float y[HT][4];
+            for (int kg = 0; kg < KG; ++kg) {
+                // two chains of products each, added at the end
+                float y[HT][4];
 #pragma unroll
-            for (int t = 0; t < HT; ++t)
+                for (int t = 0; t < HT; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[kg][t][e] = y[t][e] = 0.f;
+                    for (int e = 0; e < 4; ++e) x[kg][t][e] = y[t][e] = 0.f;
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                uint32_t f[4];
-                ldmatrix4<false>(f, kt + uint32_t(kg * 16 * RB) + k_row + (((2 * ks + k_word) ^ swz) << 4));
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    uint32_t f[4];
+                    ldmatrix4<false>(f, kt + uint32_t(kg * 16 * RB) + k_row + (((2 * ks + k_word) ^ swz) << 4));
 #pragma unroll
-                for (int t = 0; t < HT; ++t) mma16816(ks & 1 ? y[t] : x[kg][t], f, q[t][ks][0], q[t][ks][1]);
+                    for (int t = 0; t < HT; ++t) mma16816(ks & 1 ? y[t] : x[kg][t], f, q[t][ks][0], q[t][ks][1]);
+                }
+#pragma unroll
+                for (int t = 0; t < HT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[kg][t][e] = (x[kg][t][e] + y[t][e]) * a.scale;
             }
-#pragma unroll
-            for (int t = 0; t < HT; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[kg][t][e] = (x[kg][t][e] + y[t][e]) * a.scale;
         }
         // the last product with this unit's q: the next one's is on its way meanwhile
         const bool unit_end = cw.tile + 1 == cw.nt, part_end = unit_end || i + 1 == n;
@@ -470,71 +511,73 @@ paged_decode_bf16_kernel(PagedGeom geo, PdArgs a)
             nw.next<TILE>(geo, a.lens, units);
             if (part_end) load_q(nw);
         }
-        if (key0 + KT > cw.len) {
+        if (has) {
+            if (key0 + KT > cw.len) {
+#pragma unroll
+                for (int kg = 0; kg < KG; ++kg)
+#pragma unroll
+                    for (int t = 0; t < HT; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (key0 + kg * 16 + gr + (e >> 1) * 8 >= cw.len) x[kg][t][e] = -INFINITY;
+            }
+            bool lift = false;
 #pragma unroll
             for (int kg = 0; kg < KG; ++kg)
 #pragma unroll
                 for (int t = 0; t < HT; ++t)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (key0 + kg * 16 + gr + (e >> 1) * 8 >= cw.len) x[kg][t][e] = -INFINITY;
-        }
-        bool lift = false;
+                    for (int e = 0; e < 4; ++e) lift |= x[kg][t][e] > m[t][e & 1] + kPdMove;
+            if (__any_sync(0xffffffffu, lift)) {
 #pragma unroll
-        for (int kg = 0; kg < KG; ++kg)
+                for (int t = 0; t < HT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = fmaxf(x[0][t][e], x[0][t][e + 2]);
+#pragma unroll
+                        for (int kg = 1; kg < KG; ++kg) mx = fmaxf(mx, fmaxf(x[kg][t][e], x[kg][t][e + 2]));
+#pragma unroll
+                        for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+                        const float mn = fmaxf(m[t][e], mx), f = pd_weight(m[t][e], mn);
+                        m[t][e] = mn;
+                        l[t][e] *= f;
+#pragma unroll
+                        for (int dt = 0; dt < D / 16; ++dt) {
+                            o[t][dt][e] *= f;
+                            o[t][dt][e + 2] *= f;
+                        }
+                    }
+            }
+            // before any maximum is known every logit is -inf, which has no weight
+            float ref[HT][2];
 #pragma unroll
             for (int t = 0; t < HT; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) lift |= x[kg][t][e] > m[t][e & 1] + kPdMove;
-        if (__any_sync(0xffffffffu, lift)) {
+                for (int e = 0; e < 2; ++e) ref[t][e] = m[t][e] == -INFINITY ? 0.f : m[t][e];
 #pragma unroll
-            for (int t = 0; t < HT; ++t)
+            for (int kg = 0; kg < KG; ++kg) {
+                uint32_t p[HT][2];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float mx = fmaxf(x[0][t][e], x[0][t][e + 2]);
+                for (int t = 0; t < HT; ++t) {
 #pragma unroll
-                    for (int kg = 1; kg < KG; ++kg) mx = fmaxf(mx, fmaxf(x[kg][t][e], x[kg][t][e + 2]));
+                    for (int e = 0; e < 4; ++e) {
+                        const float w = ex2_approx(x[kg][t][e] - ref[t][e & 1]);
+                        l[t][e & 1] += w;
+                        x[kg][t][e] = w;
+                    }
 #pragma unroll
-                    for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-                    const float mn = fmaxf(m[t][e], mx), f = pd_weight(m[t][e], mn);
-                    m[t][e] = mn;
-                    l[t][e] *= f;
-#pragma unroll
-                    for (int dt = 0; dt < D / 16; ++dt) {
-                        o[t][dt][e] *= f;
-                        o[t][dt][e + 2] *= f;
+                    for (int e = 0; e < 2; ++e) {
+                        const __nv_bfloat162 b2 = __floats2bfloat162_rn(x[kg][t][2 * e], x[kg][t][2 * e + 1]);
+                        p[t][e] = transpose8(*reinterpret_cast<const uint32_t *>(&b2));
                     }
                 }
-        }
-        // before any maximum is known every logit is -inf, which has no weight
-        float ref[HT][2];
 #pragma unroll
-        for (int t = 0; t < HT; ++t)
+                for (int dt = 0; dt < D / 16; ++dt) {
+                    uint32_t f[4];
+                    ldmatrix4<true>(f, vt + uint32_t(kg * 16 * RB) + v_row + (((2 * dt + v_word) ^ swz) << 4));
 #pragma unroll
-            for (int e = 0; e < 2; ++e) ref[t][e] = m[t][e] == -INFINITY ? 0.f : m[t][e];
-#pragma unroll
-        for (int kg = 0; kg < KG; ++kg) {
-            uint32_t p[HT][2];
-#pragma unroll
-            for (int t = 0; t < HT; ++t) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float w = ex2_approx(x[kg][t][e] - ref[t][e & 1]);
-                    l[t][e & 1] += w;
-                    x[kg][t][e] = w;
+                    for (int t = 0; t < HT; ++t) mma16816(o[t][dt], f, p[t][0], p[t][1]);
                 }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const __nv_bfloat162 b2 = __floats2bfloat162_rn(x[kg][t][2 * e], x[kg][t][2 * e + 1]);
-                    p[t][e] = transpose8(*reinterpret_cast<const uint32_t *>(&b2));
-                }
-            }
-#pragma unroll
-            for (int dt = 0; dt < D / 16; ++dt) {
-                uint32_t f[4];
-                ldmatrix4<true>(f, vt + uint32_t(kg * 16 * RB) + v_row + (((2 * dt + v_word) ^ swz) << 4));
-#pragma unroll
-                for (int t = 0; t < HT; ++t) mma16816(o[t][dt], f, p[t][0], p[t][1]);
             }
         }
         __syncwarp();   // the stage may be refilled
@@ -550,10 +593,11 @@ paged_decode_bf16_kernel(PagedGeom geo, PdArgs a)
                     for (int w = 4; w < 32; w <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], w);
                     const int j = 8 * t + 2 * tc + e;
                     if (gr == 0) red_ml[warp][j] = make_float2(m[t][e], l[t][e]);
+                    if (l[t][e] == 0.f) continue;
 #pragma unroll
                     for (int dt = 0; dt < D / 16; ++dt) {
-                        red_o[(warp * HB + j) * D + dt * 16 + gr] = o[t][dt][e];
-                        red_o[(warp * HB + j) * D + dt * 16 + gr + 8] = o[t][dt][e + 2];
+                        red_o[(warp * HB + j) * (D + kPdPad) + dt * 16 + gr] = o[t][dt][e];
+                        red_o[(warp * HB + j) * (D + kPdPad) + dt * 16 + gr + 8] = o[t][dt][e + 2];
                     }
                 }
             __syncthreads();
@@ -665,7 +709,7 @@ template <typename T, int D, int HB>
 cudaError_t run(void (*kern)(PagedGeom, PdArgs), const PagedGeom &g, PdArgs a, cudaStream_t st)
 {
     a.chunks = (g.g + HB - 1) / HB;
-    const size_t smem = size_t(kPdWarps) * kPdStages * kPdStage + size_t(kPdWarps) * HB * D * 4;
+    const size_t smem = size_t(kPdWarps) * kPdStages * kPdStage + size_t(kPdWarps) * HB * (D + kPdPad) * 4;
     // one range per CTA that the SMs hold at once
     const int ranges = num_sms() * int(std::min<size_t>(kPdResident, 228 * 1024 / (smem + 2048)));
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));

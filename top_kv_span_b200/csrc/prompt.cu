@@ -29,7 +29,7 @@ constexpr int kPrGroup = kPrRows / 4 * 16;   // threads of a group
 // Padded rows: a column of them falls into different banks.  Q, then K, V and P of
 // every group, as many groups as fit.
 template <int D> struct PrSmem {
-    static constexpr int kGroups = D == 64 ? 4 : 2;
+    static constexpr int kGroups = D == 64 ? 4 : 1;
     static constexpr int RS = D + 4, PS = kPrKeys + 4;
     static constexpr int oK = 0, oV = oK + kPrKeys * RS, oP = oV + kPrKeys * RS,
                          kOne = oP + kPrRows * PS, oGroups = kPrRows * RS;

@@ -10,9 +10,10 @@
 // Every byte is read and written once, so memory bounds it: a block takes a few
 // tokens, forms their d/2 angles once in shared memory (all heads of a token
 // share them) and then moves 16-byte words.  16001 tokens of 32/8 heads of width 128
-// take 80 us, 5.3 TB/s (82% of the copy bandwidth); blocks of 128 or 512 threads 84
-// and 80, 8 tokens a block 84, streaming cache hints 82, the data loads ahead of the
-// lookups 88.  A call of one token takes 4 us of the GPU.
+// take 79 us, 5.4 TB/s (84% of the copy bandwidth).  Against 80.5 us before it was
+// launched beside the end of its predecessor: blocks of 128 or 512 threads 84 and 80,
+// 8 tokens a block 84, streaming cache hints 82, the data loads ahead of the lookups 88.
+// A call of one token takes 4 us of the GPU.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

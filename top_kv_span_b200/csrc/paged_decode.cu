@@ -9,9 +9,11 @@
 // 16-byte asynchronous copies and never waits for the other warps until a unit
 // ends; rows past the sequence, or on a page that the table does not name, are
 // filled with zeros in shared memory, so nothing there can reach a sum.
-// One sequence of 131073 tokens, 32/8 heads of width 128 in bf16, takes 94 us, 5.7 TB/s
-// (89% of the copy bandwidth, the join and both launches included); 61 sequences of up
-// to 8K 96 us (92%); 256 of 1.5K tokens with 12/2 heads 76 us (84%).
+// One sequence of 131073 tokens, 32/8 heads of width 128 in bf16, takes 90 us, 5.95 TB/s
+// (92% of the copy bandwidth, the join and both launches included); 61 sequences of up
+// to 8K 96 us (92%); 256 of 1.5K tokens with 12/2 heads 75 us (85%).  Where units hold
+// few keys their ends bound it: 256 sequences of 31 tokens, 25 us (32 before warps
+// without keys passed a tile over and the warps' sums were joined four at a time).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -410,7 +412,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x)
 // exceeds it by 2^8, so most tiles need no reduction over the keys.
 // Memory bounds it, once enough warps hide the chain of one tile (paged_decode.cuh has
 // the shapes measured); the same walk on the CUDA cores took 163, 168 and 194 us where
-// this takes 94, 96 and 76.
+// this takes 90, 96 and 75.
 constexpr float kPdMove = 8.f;
 template <int D, int HT>
 __global__ void __launch_bounds__(kPdThreads)

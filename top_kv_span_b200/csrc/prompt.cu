@@ -10,9 +10,11 @@
 // operand at a time from shared memory.  A group's next K tile loads during P.V and its
 // next V tile during Q.K^T.  The arithmetic is fp32 multiply-adds; what bounds it are the
 // registers' fills from shared memory, eight 16-byte loads for 64 multiply-adds of a
-// thread.  Two prompts of 4131 tokens together, 4/1 heads of width 64, take 162 us,
-// 29 TFLOP/s (one group of four warps per CTA 225 us; on the tensor cores with operands
-// split in two tf32 terms 160 us, at three times the error).
+// thread.  Two prompts of 4131 tokens together, 4/1 heads of width 64, take 159 us,
+// 29 TFLOP/s (one group of four warps per CTA 210 us; on the tensor cores with operands
+// split in two tf32 terms the same, at three times the error).  Width 128 leaves room
+// for two groups in one CTA or for two CTAs of one, which is faster: a prompt of 2000
+// tokens with 32/8 heads 988 us against 1102, five of 423 together 36 against 50.
 #include <cuda_runtime.h>
 #include <math.h>
 

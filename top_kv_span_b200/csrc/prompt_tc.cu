@@ -27,13 +27,14 @@
 // next block's loads and first S run during the last steps and the stores of this one.
 // What bounds it: the exponentials, 128 x 64 a tile and step at 16 per clock and SM,
 // as long as the products take, and what the softmax warps do besides; in long runs the
-// power limit.  A prompt of 16384 tokens, 32/8 heads of width 128, takes 1.73 ms by itself
-// and 2.0 ms in a loop (1.27 and 1.1 PFLOP/s), seven prompts of 8191 tokens together
-// 131 us.  Measured and dropped, on the way there (16384 tokens, in a loop): 128-key
-// steps with one S buffer per tile, the other way to fill the 512 TMEM columns, which
-// leave the chain S -> softmax -> P.V -> S open (2.22 ms); two threads per row (2.63 ms); a
-// quarter of the exponentials as a polynomial on the FMA pipe (2.05 ms, against 2.01);
-// one block per CTA, whose loads and stores stand alone (152 us for the seven prompts).
+// power limit.  A prompt of 16384 tokens, 32/8 heads of width 128, takes 1.67 ms by itself
+// and 1.95 ms in a loop (1.32 and 1.13 PFLOP/s), seven prompts of 8191 tokens together
+// 126 us.  Measured and dropped, on the way there (16384 tokens, in a loop, against what
+// stood then): 128-key steps with one S buffer per tile, the other way to fill the 512
+// TMEM columns, which leave the chain S -> softmax -> P.V -> S open (2.22 ms, 2.01); two
+// threads per row (2.63 ms, 2.31); a quarter of the exponentials as a polynomial on the
+// FMA pipe (2.05 ms, 2.01); S loaded a step ahead, which spills (3.18 ms, 2.07); one
+// block per CTA, whose loads and stores stand alone (152 us for the seven prompts, 133).
 // The logits are exact products summed in fp32; P rounds to bf16 (its operand
 // type; the row sum takes the unrounded value), O is summed in fp32.
 //

@@ -242,15 +242,18 @@ paged_decode_f32_kernel(PagedGeom geo, PdArgs a)
     const int units = geo.Hkv * a.chunks;
     pdl_trigger();   // the join may be scheduled; it waits for this grid's end
     pdl_wait();
-    pd_empty<float, D>(geo, a);
     PdWalk cw;
     const int64_t n = pd_range<TILE>(geo, a.lens, units, cw);
     if (tid == 0) a.meta[blockIdx.x] = PdMeta{-1, 0, 0, 0};
-    if (n == 0) return;
+    if (n == 0) {
+        pd_empty<float, D>(geo, a);
+        return;
+    }
     const uint8_t *ring = smem + warp * kPdStages * kPdStage;
     Stream stream(geo, a, cw, n, units, smem_addr(ring));
 #pragma unroll
     for (int s = 0; s < kPdStages - 1; ++s) stream.load();
+    pd_empty<float, D>(geo, a);   // behind the first loads
 
     float qv[HB][E], o[HB][E], m, l;   // m, l: of head lane % HB
     auto load_q = [&](const PdWalk &w) {
@@ -430,15 +433,18 @@ paged_decode_bf16_kernel(PagedGeom geo, PdArgs a)
     const int units = geo.Hkv * a.chunks;
     pdl_trigger();   // the join may be scheduled; it waits for this grid's end
     pdl_wait();
-    pd_empty<uint16_t, D>(geo, a);
     PdWalk cw;
     const int64_t n = pd_range<TILE>(geo, a.lens, units, cw);
     if (tid == 0) a.meta[blockIdx.x] = PdMeta{-1, 0, 0, 0};
-    if (n == 0) return;
+    if (n == 0) {
+        pd_empty<uint16_t, D>(geo, a);
+        return;
+    }
     const uint32_t ring = smem_addr(smem + warp * kPdStages * kPdStage);
     Stream stream(geo, a, cw, n, units, ring);
 #pragma unroll
     for (int s = 0; s < kPdStages - 1; ++s) stream.load();
+    pd_empty<uint16_t, D>(geo, a);   // behind the first loads
 
     // this lane's rows for ldmatrix, and the swizzle of its words
     const uint32_t k_row = uint32_t((lane & 15) * RB), v_row = uint32_t(((lane & 7) + (lane >> 4) * 8) * RB);
@@ -625,41 +631,57 @@ paged_decode_join_kernel(PagedGeom geo, PdArgs a)
     __shared__ int last_s;
     __shared__ float top[HB], total[HB], weight[kJoinParts][HB];
     __shared__ float4 sums[kJoinThreads];
-    const int tid = threadIdx.x, n = gridDim.x, first = blockIdx.x;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = gridDim.x, first = blockIdx.x;
     if (tid == 0) last_s = n - 1;
+    __syncthreads();
     pdl_wait();
-    __syncthreads();
-    // the range that ends the unit: the first one after this whose slot says so
-    const PdMeta me = a.meta[first];
-    for (int i = first + 1 + tid; i < n; i += kJoinThreads)
-        if (a.meta[i].first == 1) atomicMin(&last_s, i);
-    if (me.open_b < 0) return;
-    __syncthreads();
-    const int parts = last_s - first + 1;
     // partial x is range first + x's: its last slot for x = 0, else its first one
     auto slot_of = [&](int x) { return x == 0 ? 2 * first + 1 : 2 * (first + x); };
+    // What the next lines may need, all on its way at once: what this range left, which
+    // later range ends the unit (the first one whose slot says so), and the first
+    // partials' maxima and sums, a warp per head (of ranges that exist, used or not)
+    const PdMeta me = a.meta[first];
+    bool ends = false;
+    if (first + 1 + tid < n) ends = a.meta[first + 1 + tid].first == 1;
+    float2 pre[kJoinParts / 32];
+#pragma unroll
+    for (int u = 0; u < kJoinParts / 32; ++u) {
+        const int x = u * 32 + lane;
+        pre[u] = warp < HB && first + x < n ? a.part_ml[slot_of(x) * HB + warp] : make_float2(0.f, 0.f);
+    }
+    if (me.open_b < 0) return;
+    if (ends) atomicMin(&last_s, first + 1 + tid);
+    for (int i = first + 1 + kJoinThreads + tid; i < n; i += kJoinThreads)
+        if (a.meta[i].first == 1) atomicMin(&last_s, i);
+    __syncthreads();
+    const int parts = last_s - first + 1;
     const int h = me.open_u / a.chunks, j0 = (me.open_u % a.chunks) * HB;
     const int nh = min(HB, geo.g - j0);
-    // the joint maximum and sum of each head, a warp per head
-    for (int j = tid >> 5; j < nh; j += kJoinThreads / 32) {
-        const int lane = tid & 31;
+    // the joint maximum and sum of each head, and the first partials' weights
+    if (warp < nh) {
         float M = -INFINITY, L = 0.f;
-        for (int x = lane; x < parts; x += 32) {
-            const float2 ml = a.part_ml[slot_of(x) * HB + j];
+        auto take = [&](const float2 &ml) {
             const float mn = fmaxf(M, ml.x);
             L = L * pd_weight(M, mn) + pd_weight(ml.x, mn) * ml.y;
             M = mn;
-        }
-        float top_m = M;
+        };
 #pragma unroll
-        for (int w = 16; w; w >>= 1) top_m = fmaxf(top_m, __shfl_xor_sync(0xffffffffu, top_m, w));
-        L *= pd_weight(M, top_m);
+        for (int u = 0; u < kJoinParts / 32; ++u)
+            if (u * 32 + lane < parts) take(pre[u]);
+        for (int x = kJoinParts + lane; x < parts; x += 32) take(a.part_ml[slot_of(x) * HB + warp]);
+        float all = M;
+#pragma unroll
+        for (int w = 16; w; w >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, w));
+        L *= pd_weight(M, all);
 #pragma unroll
         for (int w = 16; w; w >>= 1) L += __shfl_xor_sync(0xffffffffu, L, w);
         if (lane == 0) {
-            top[j] = top_m;
-            total[j] = L;
+            top[warp] = all;
+            total[warp] = L;
         }
+#pragma unroll
+        for (int u = 0; u < kJoinParts / 32; ++u)
+            if (u * 32 + lane < parts) weight[u * 32 + lane][warp] = pd_weight(pre[u].x, all);
     }
     // groups of threads, one float4 word of the heads a thread
     const int words = nh * D / 4, groups = kJoinThreads / words, group = tid / words, word = tid % words;
@@ -668,11 +690,13 @@ paged_decode_join_kernel(PagedGeom geo, PdArgs a)
     for (int x0 = 0; x0 < parts; x0 += kJoinParts) {
         const int np = min(kJoinParts, parts - x0);
         __syncthreads();
-        for (int y = tid; y < np * nh; y += kJoinThreads) {
-            const int x = y / nh, i = y - x * nh;
-            weight[x][i] = pd_weight(a.part_ml[slot_of(x0 + x) * HB + i].x, top[i]);
+        if (x0 > 0) {
+            for (int y = tid; y < np * nh; y += kJoinThreads) {
+                const int x = y / nh, i = y - x * nh;
+                weight[x][i] = pd_weight(a.part_ml[slot_of(x0 + x) * HB + i].x, top[i]);
+            }
+            __syncthreads();
         }
-        __syncthreads();
         if (group < groups)
 #pragma unroll 8
             for (int x = group; x < np; x += groups) {

@@ -736,7 +736,9 @@ cudaError_t run(void (*kern)(PagedGeom, PdArgs), const PagedGeom &g, PdArgs a, c
 {
     a.chunks = (g.g + HB - 1) / HB;
     const size_t smem = size_t(kPdWarps) * kPdStages * kPdStage + size_t(kPdWarps) * HB * (D + kPdPad) * 4;
-    // one range per CTA that the SMs hold at once
+    // one range per CTA that the SMs hold at once (two, three or four, handed out as CTAs
+    // end, even out SMs of different speed but cost more starts and partials: 97, 102 and
+    // 109 us where one takes 88, one sequence of 131073 tokens)
     const int ranges = num_sms() * int(std::min<size_t>(kPdResident, 228 * 1024 / (smem + 2048)));
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;

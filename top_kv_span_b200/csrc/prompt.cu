@@ -3,7 +3,7 @@
 //   o_i = sum_{t <= i} softmax_t(q_i.k_t / sqrt(d)) v_t   within each sequence
 //
 // One CTA takes 32 consecutive tokens of one query head.  Its groups of four warps
-// walk the keys 64 at a time in turn, each with a running maximum and sum of the
+// (four of them at width 64, one at 128) walk the keys 64 at a time in turn, each with a running maximum and sum of the
 // softmax of its own, and join at the end, so that an SM works on few blocks at a time
 // and the longest one does not outlast the others.  Scores and output stay in registers
 // (4 x 4 and 4 x d/16 per thread), and both products read four elements of either

@@ -388,7 +388,8 @@ REATT_API int reatt_paged_append(const reatt_paged_dims *dims, const void *q, co
  * with head j on KV head j / (Hq / Hkv).  q: row b is sequence b's token,
  * rotated already (N = B); its own key and value are in the cache, appended
  * before.  out [B, Hq, d], dense.  seq_len[b] = 0 gives zeros.  fp32 softmax
- * and accumulation; slots past seq_len are never used, whatever they hold.
+ * and accumulation (bf16: a weight meets V as two bf16 terms, good to 2^-14);
+ * slots past seq_len are never used, whatever they hold.
  */
 REATT_API int reatt_paged_decode(const reatt_paged_dims *dims, const void *q, const void *k_pages,
                                  const void *v_pages, const int32_t *page_table,

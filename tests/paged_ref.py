@@ -23,9 +23,10 @@ def rotate(x, pos, base):
     return y, torch.cat([s, s], -1) + half_step(x.dtype) * y.abs()
 
 
-def attend(q, k, v, last):
+def attend(q, k, v, last, p_step=None):
     """q [Hq, n, d] over k, v [Hkv, m, d]; row r sees keys 0..last[r] ->
-    (out [Hq, n, d], bound).  k, v are taken only where some row sees them."""
+    (out [Hq, n, d], bound).  k, v are taken only where some row sees them.  p_step:
+    how far a weight may be rounded before it meets v (half a step of bf16 for bf16)."""
     Hq, n, d = q.shape
     g, m = Hq // k.shape[0], k.shape[1]
     dt = q.dtype
@@ -50,7 +51,7 @@ def attend(q, k, v, last):
     pv = p @ vv.abs()
     tol = (2 * e + (m + 8) * 2.0 ** -23) * pv + half_step(dt) * o.abs()
     if dt != torch.float32:
-        tol = tol + half_step(dt) * pv
+        tol = tol + (half_step(dt) if p_step is None else p_step) * pv
     return o, tol * (1 + 2.0 ** -6) + 1e-30
 
 

@@ -161,6 +161,52 @@ def test_decode_bad_pages_and_lengths_are_left_out(R):
         assert call(pool.table, [100, 60, 30, 20]) == R.OK
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(4, 1), (16, 2), (40, 2)])
+def test_decode_weights_keep_their_precision(R, Hq, Hkv, d):
+    """bf16: a weight meets v as a sum of two bf16 terms.  The first is cut off, within
+    2^-7 of the weight, the second is off by 2^-8 of that and has 2^-16 of the weight
+    added: under 2^-14.  Sums of many values of either sign show it: they are much
+    smaller than their terms."""
+    lens = [150, 33, 7, 1, 90]
+    pool = ref.Pool(lens, Hkv, d, 16, BF16, 71)
+    q = torch.randn((len(lens), Hq, d), generator=torch.Generator().manual_seed(72)).to(BF16)
+    dims = R.make_paged_dims(B=len(lens), Hq=Hq, Hkv=Hkv, d=d, dtype=BF16, N=len(lens), page=16,
+                             max_pages=pool.max_pages, n_pages=pool.n_pages)
+    out = torch.empty((len(lens), Hq, d), dtype=BF16, device="cuda")
+    R.reatt_paged_decode(dims, q.cuda(), pool.k.cuda(), pool.v.cuda(), pool.table.cuda(), ints(lens),
+                         out, workspace(R, dims))
+    for b, n in enumerate(lens):
+        k, v = (x.transpose(0, 1) for x in pool.rows[b])
+        o, tol = ref.attend(q[b].unsqueeze(1), k, v, torch.tensor([n - 1]), p_step=2.0 ** -14)
+        ref.check(out[b].cpu(), o[:, 0], tol[:, 0], f"sequence {b} of {n}")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("what", [math.inf, -math.inf])
+def test_decode_infinite_value_stays_infinite(R, dtype, what):
+    """An infinity in V that the token sees has a weight above zero: the column is that
+    infinity; other columns and sequences are as without it."""
+    for lens, at in (([50, 50], 7), ([3000, 50], 2999), ([3000, 50], 16)):
+        pool = ref.Pool(lens, 2, 128, 16, dtype, 6)
+        q = torch.randn((2, 8, 128), generator=torch.Generator().manual_seed(3)).to(dtype)
+        dims = R.make_paged_dims(B=2, Hq=8, Hkv=2, d=128, dtype=dtype, N=2, page=16,
+                                 max_pages=pool.max_pages, n_pages=pool.n_pages)
+        ws, outs = workspace(R, dims), []
+        for _ in range(2):
+            out = torch.empty((2, 8, 128), dtype=dtype, device="cuda")
+            R.reatt_paged_decode(dims, q.cuda(), pool.k.cuda(), pool.v.cuda(), pool.table.cuda(),
+                                 ints(lens), out, ws)
+            outs.append(out)
+            v = pool.rows[0][1][at:at + 1].clone()
+            v[0, :, 5] = what
+            pool.put(0, at, pool.rows[0][0][at:at + 1], v)
+        clean, got = outs
+        assert (got[0, :, 5] == what).all()
+        got[0, :, 5] = clean[0, :, 5]
+        assert torch.equal(got, clean)
+
+
 # ------------------------------------------------------------------ append
 def run_append(R, Hq, Hkv, d, dtype, page, past, new, base, *, keep_k=True, in_place=False,
                fused=True, before=0, after=0, with_q=True, seed=1):

@@ -410,13 +410,18 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x)
 // groups): S^T = K.Q^T, 16 keys x 8 heads, and O^T += V^T.P^T, 16 elements of d x 8
 // heads.  K and V come by ldmatrix from rows whose 16-byte words are swizzled by
 // the row's low three bits (no bank conflicts), S^T turns into the operand P^T by
-// 8 x 8 transposes between registers, P rounds to bf16 there (the row sum takes the
-// unrounded value).  The reference maximum of a head moves only when some logit
+// 8 x 8 transposes between registers.  P stays a sum of two bf16 terms, the value cut
+// off and what that left (up to 2^-7, rounded by 2^-8 of it: together good to 2^-14, so
+// the row sum may take the fp32 value), at two products: one bf16 term makes the result's
+// error 1.1 to 1.5 times that of its own rounding and is no faster (89, 96 and 75 us; two 89, 96 and 76).  Both terms
+// are above zero where the weight is (kPdMore sees to the second), so that an infinity in
+// V stays one.  The reference maximum of a head moves only when some logit
 // exceeds it by 2^8, so most tiles need no reduction over the keys.
 // Memory bounds it, once enough warps hide the chain of one tile (paged_decode.cuh has
 // the shapes measured); the same walk on the CUDA cores took 163, 168 and 194 us where
 // this takes 90, 96 and 75.
 constexpr float kPdMove = 8.f;
+constexpr float kPdMore = 1.f / (1 << 16);   // of the weight, added to its second term
 template <int D, int HT>
 __global__ void __launch_bounds__(kPdThreads)
 paged_decode_bf16_kernel(PagedGeom geo, PdArgs a)
@@ -564,7 +569,7 @@ paged_decode_bf16_kernel(PagedGeom geo, PdArgs a)
                 for (int e = 0; e < 2; ++e) ref[t][e] = m[t][e] == -INFINITY ? 0.f : m[t][e];
 #pragma unroll
             for (int kg = 0; kg < KG; ++kg) {
-                uint32_t p[HT][2];
+                uint32_t p[HT][2], rest[HT][2];   // P = p + rest, to 2^-14
 #pragma unroll
                 for (int t = 0; t < HT; ++t) {
 #pragma unroll
@@ -575,8 +580,12 @@ paged_decode_bf16_kernel(PagedGeom geo, PdArgs a)
                     }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const __nv_bfloat162 b2 = __floats2bfloat162_rn(x[kg][t][2 * e], x[kg][t][2 * e + 1]);
-                        p[t][e] = transpose8(*reinterpret_cast<const uint32_t *>(&b2));
+                        const float w0 = x[kg][t][2 * e], w1 = x[kg][t][2 * e + 1];
+                        const uint32_t hi = __byte_perm(__float_as_uint(w0), __float_as_uint(w1), 0x7632);
+                        const __nv_bfloat162 r2 = __floats2bfloat162_rn(
+                            fmaf(w0, kPdMore, w0 - bf16lo(hi)), fmaf(w1, kPdMore, w1 - bf16hi(hi)));
+                        p[t][e] = transpose8(hi);
+                        rest[t][e] = transpose8(*reinterpret_cast<const uint32_t *>(&r2));
                     }
                 }
 #pragma unroll
@@ -584,7 +593,10 @@ paged_decode_bf16_kernel(PagedGeom geo, PdArgs a)
                     uint32_t f[4];
                     ldmatrix4<true>(f, vt + uint32_t(kg * 16 * RB) + v_row + (((2 * dt + v_word) ^ swz) << 4));
 #pragma unroll
-                    for (int t = 0; t < HT; ++t) mma16816(o[t][dt], f, p[t][0], p[t][1]);
+                    for (int t = 0; t < HT; ++t) {
+                        mma16816(o[t][dt], f, p[t][0], p[t][1]);
+                        mma16816(o[t][dt], f, rest[t][0], rest[t][1]);
+                    }
                 }
             }
         }

@@ -401,8 +401,10 @@ REATT_API int reatt_paged_decode(const reatt_paged_dims *dims, const void *q, co
  *   out[i,j] = sum_{t <= i, same sequence} softmax_t(q[i,j] . k[t] / sqrt(d)) v[t]
  * with head j on KV head j / (Hq / Hkv), q and k rotated already (the rotated
  * copies of reatt_paged_append).  out [N, Hq, d], dense.  fp32 softmax and
- * accumulation.  A token never reads a later token or another sequence,
- * whatever those rows hold.  The page fields of dims are not used.
+ * accumulation (bf16: a weight is rounded to bf16 before it meets V and before it
+ * is summed, so the weights that V meets sum to one).  A token never reads a
+ * later token or another sequence, whatever those rows hold.  The page fields of
+ * dims are not used.
  */
 REATT_API int reatt_prompt_attend(const reatt_paged_dims *dims, const void *q, const void *k,
                                   const void *v, const int32_t *cu_seqlens, void *out, void *ws,

@@ -485,6 +485,42 @@ def test_prompt_logits_of_minus_infinity(R):
         assert out.isnan().all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_of_equal_values_returns_them(R, d):
+    """Weights that sum to one give back a value that all tokens share: the sums in fp32
+    are off by (m + 8) steps of 2^-23 at most, each, which is far from half a step."""
+    lens = [1, 2, 5, 64, 65, 130, 300]
+    gen = torch.Generator().manual_seed(81)
+    N = sum(lens)
+    q, k = (torch.randn((N, h, d), generator=gen).mul(1.5).to(BF16).cuda() for h in (8, 2))
+    v = torch.cat([torch.randn((1, 2, d), generator=gen).to(BF16).expand(n, 2, d) for n in lens]).cuda()
+    dims = R.make_paged_dims(B=len(lens), Hq=8, Hkv=2, d=d, dtype=BF16, N=N)
+    out = torch.empty_like(q)
+    R.reatt_prompt_attend(dims, q, k, v, ints(starts(lens)), out, workspace(R, dims))
+    assert torch.equal(out, v.repeat_interleave(4, 1))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_rounded_weights_still_sum_to_one(R, d):
+    """bf16: rounding a weight p_t by half a step moves the row by that of p_t (v_t - o)
+    only, as the sum takes the rounded weights: little where the values are alike."""
+    n, Hq = 150, 4
+    gen = torch.Generator().manual_seed(82)
+    q, k, v = (torch.randn((n, h, d), generator=gen) for h in (Hq, 1, 1))
+    q, k, v = q.to(BF16), k.to(BF16), (4 + v / 32).to(BF16)
+    dims = R.make_paged_dims(B=1, Hq=Hq, Hkv=1, d=d, dtype=BF16, N=n)
+    out = torch.empty((n, Hq, d), dtype=BF16, device="cuda")
+    R.reatt_prompt_attend(dims, q.cuda(), k.cuda(), v.cuda(), ints([0, n]), out, workspace(R, dims))
+    qt, kt, vt = (x.transpose(0, 1) for x in (q, k, v))
+    o, tol = ref.attend(qt, kt, vt, torch.arange(n), p_step=0.0)
+    x = (qt.double() @ kt.double().transpose(-1, -2)) / math.sqrt(d)
+    p = torch.softmax(x.masked_fill(torch.ones(n, n).triu(1) > 0, -math.inf), -1)
+    apart = torch.stack([(p[:, r, :, None] * (vt.double() - o[:, r, None]).abs()).sum(1)
+                         for r in range(n)], 1)
+    tol = tol + 2.0 ** -8 * (1 + 2.0 ** -6) * apart
+    ref.check(out.cpu(), o.transpose(0, 1), tol.transpose(0, 1))
+
+
 def test_prompt_malformed_offsets_stay_inside(R):
     q = torch.randn((60, 4, 64), device="cuda").to(BF16)
     k = torch.randn((60, 1, 64), device="cuda").to(BF16)

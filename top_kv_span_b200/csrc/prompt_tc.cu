@@ -27,16 +27,20 @@
 // next block's loads and first S run during the last steps and the stores of this one.
 // What bounds it: the exponentials, 128 x 64 a tile and step at 16 per clock and SM,
 // as long as the products take, and what the softmax warps do besides; in long runs the
-// power limit.  A prompt of 16384 tokens, 32/8 heads of width 128, takes 1.67 ms by itself
-// and 1.95 ms in a loop (1.32 and 1.13 PFLOP/s), seven prompts of 8191 tokens together
-// 126 us.  Measured and dropped, on the way there (16384 tokens, in a loop, against what
+// power limit.  A prompt of 16384 tokens, 32/8 heads of width 128, takes 1.76 ms by itself
+// and 2.03 ms in a loop (1.25 and 1.08 PFLOP/s), seven prompts of 8191 tokens together
+// 128 us.  Measured and dropped, on the way there (16384 tokens, in a loop, against what
 // stood then): 128-key steps with one S buffer per tile, the other way to fill the 512
 // TMEM columns, which leave the chain S -> softmax -> P.V -> S open (2.22 ms, 2.01); two
 // threads per row (2.63 ms, 2.31); a quarter of the exponentials as a polynomial on the
 // FMA pipe (2.05 ms, 2.01); S loaded a step ahead, which spills (3.18 ms, 2.07); one
 // block per CTA, whose loads and stores stand alone (152 us for the seven prompts, 133).
-// The logits are exact products summed in fp32; P rounds to bf16 (its operand
-// type; the row sum takes the unrounded value), O is summed in fp32.
+// The logits are exact products summed in fp32; P rounds to bf16 (its operand type), O is
+// summed in fp32, and so is the row sum, of the rounded values: a weight's rounding then
+// moves a row by its share of v - o, not of v (error against 64 bits of the seven prompts
+// 0.0021 -> 0.0019, the fp32 form's 0.0016; values that all tokens share come back exact).
+// Summing the unrounded values took 125 us and 1.96 ms, this 128 us and 2.03 ms (with the
+// halves widened by integer instructions 133 us and 2.13 ms).
 //
 // Values behind the mask: a masked S is replaced before it is used, but a masked
 // P = 0 still meets its V row in the product, so in the steps that hold any
@@ -150,6 +154,14 @@ __device__ __forceinline__ bool elect_one()
     uint32_t e;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
     return e != 0;
+}
+// Adds the two bf16 values of a word to two fp32 sums, exactly widened.
+__device__ __forceinline__ void add_bf16x2(float &a, float &b, uint32_t w)
+{
+    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\t"
+        "add.rn.f32.bf16 %0, x, %0;\n\tadd.rn.f32.bf16 %1, y, %1;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "r"(w));
 }
 __device__ __forceinline__ bool bf16x2_odd(uint32_t w)   // an infinity or NaN in either half
 {
@@ -548,7 +560,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 fine = my_turn(j) && fine;
                 __syncwarp();
                 const uint64_t sc2 = pack2(scale, scale), mc2 = pack2(-mc, -mc);
-                uint64_t sum[4] = {0, 0, 0, 0};
+                float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     uint32_t w[16];
@@ -559,9 +571,9 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                         unpack2(x, p0, p1);
                         p0 = ex2_approx(p0);
                         p1 = ex2_approx(p1);
-                        sum[i & 3] = add2(sum[i & 3], pack2(p0, p1));
                         const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
                         w[i] = *reinterpret_cast<const uint32_t *>(&b2);
+                        add_bf16x2(sum[2 * (i & 3)], sum[2 * (i & 3) + 1], w[i]);
                     }
                     tmem_st16_nowait(t_s + uint32_t(c * 16), w);
                     if (c == 0) pass_on();   // half way, so that the hand-over costs no pause
@@ -570,10 +582,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 tc_fence_before();
                 if (!__all_sync(0xffffffffu, fine)) return false;
                 if (lane == 0) mbar_arrive(&sh.pfull[t][g & 1]);
-                const uint64_t l2 = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-                float l0, l1;
-                unpack2(l2, l0, l1);
-                l += l0 + l1;
+                l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
                 return true;
             };
             int j = 0;

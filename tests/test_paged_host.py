@@ -160,3 +160,147 @@ def test_unknown_dtypes_are_refused(R):
             dims(R, dtype=dtype)
         assert e.value.code == R.EUNSUPPORTED
     assert dims(R, dtype=torch.float32).dtype == R.F32 and dims(R, dtype="bf16").dtype == R.BF16
+
+
+# ------------------------------------------------------------------ the binding's look at tensors
+@pytest.fixture
+def on_host(R, monkeypatch):
+    """The binding with the host as its device and calls that only note their arguments."""
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)   # get_device() of a host tensor
+    R._paged_plan.cache_clear()
+    calls = []
+    for name in ("reatt_paged_append", "reatt_paged_decode", "reatt_prompt_attend"):
+        monkeypatch.setattr(R.lib, name, lambda *a: calls.append(a) or R.OK)
+    yield calls
+    R._paged_plan.cache_clear()
+
+
+B, HQ, HKV, D, PAGE, PAGES, COLS, ROWS = 3, 8, 2, 64, 16, 11, 4, 20
+
+
+def operands(call, dtype=torch.bfloat16):
+    """Well-formed operands of a call, q, k and v as slices of one projection."""
+    N = B if call == "decode" else ROWS
+    row = torch.zeros((N, HQ + 2 * HKV, D), dtype=dtype)
+    i32 = torch.int32
+    x = dict(q=row[:, :HQ], k=row[:, HQ:HQ + HKV], v=row[:, HQ + HKV:],
+             cu=torch.zeros(B + 1, dtype=i32), past=torch.zeros(B, dtype=i32),
+             table=torch.zeros((B, COLS), dtype=i32), q_rot=torch.zeros((N, HQ, D), dtype=dtype),
+             k_rot=torch.zeros((N, HKV, D), dtype=dtype),
+             k_pages=torch.zeros((PAGES, HKV, PAGE, D), dtype=dtype),
+             v_pages=torch.zeros((PAGES, HKV, PAGE, D), dtype=dtype),
+             lens=torch.zeros(B, dtype=i32), out=torch.zeros((N, HQ, D), dtype=dtype))
+    return x
+
+
+def call_with(R, call, x, dtype="bf16", **kw):
+    s = (HQ + 2 * HKV) * D
+    d = R.make_paged_dims(B=B, Hq=HQ, Hkv=HKV, d=D, dtype=dtype, N=B if call == "decode" else ROWS,
+                          page=PAGE, max_pages=COLS, n_pages=PAGES, q_stride=s, k_stride=s,
+                          v_stride=s, **kw)
+    if "ws" not in x:
+        x = dict(x, ws=torch.zeros(R.reatt_paged_workspace_bytes(d), dtype=torch.uint8))
+    if call == "append":
+        return R.reatt_paged_append(d, x["q"], x["k"], x["v"], x["cu"], x["past"], x["table"],
+                                    x["q_rot"], x["k_rot"], x["k_pages"], x["v_pages"], x["lens"],
+                                    x["ws"], stream=0)
+    if call == "decode":
+        return R.reatt_paged_decode(d, x["q"], x["k_pages"], x["v_pages"], x["table"], x["lens"],
+                                    x["out"], x["ws"], stream=0)
+    return R.reatt_prompt_attend(d, x["q"], x["k"], x["v"], x["cu"], x["out"], x["ws"], stream=0)
+
+
+CALLS = {"append": ("q", "k", "v", "cu", "past", "table", "q_rot", "k_rot", "k_pages", "v_pages", "lens"),
+         "decode": ("q", "k_pages", "v_pages", "table", "lens", "out"),
+         "prompt": ("q", "k", "v", "cu", "out")}
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_well_formed_tensors_pass_with_their_addresses(R, on_host, call):
+    x = operands(call)
+    for _ in range(2):
+        assert call_with(R, call, x) == R.OK
+    got = on_host[-1][1:]
+    order = {"append": ("q", "k", "v", "cu", "past", "table", "q_rot", "k_rot", "k_pages", "v_pages", "lens"),
+             "decode": ("q", "k_pages", "v_pages", "table", "lens", "out"),
+             "prompt": ("q", "k", "v", "cu", "out")}[call]
+    assert list(got[:len(order)]) == [x[n].data_ptr() for n in order]
+
+
+@pytest.mark.parametrize("call,name", [(c, n) for c in CALLS for n in CALLS[c]])
+@pytest.mark.parametrize("after", [False, True])
+def test_short_tensors_are_refused(R, on_host, call, name, after):
+    """One row, page or entry too few would be read or written past its end; also after
+    a call whose operands fitted."""
+    x = operands(call)
+    if after:
+        call_with(R, call, x)
+    short = x[name][:-1]
+    with pytest.raises(R.ReattError) as e:
+        call_with(R, call, dict(x, **{name: short}))
+    assert e.value.code == R.EINVAL
+    assert call_with(R, call, x) == R.OK
+
+
+@pytest.mark.parametrize("call,name", [(c, n) for c in CALLS for n in CALLS[c]])
+@pytest.mark.parametrize("after", [False, True])
+def test_other_layouts_are_refused(R, on_host, call, name, after):
+    """The same elements in another order: transposed, every second one, or dense rows
+    where the dims say that they lie apart."""
+    x = operands(call)
+    if after:
+        call_with(R, call, x)
+    t = x[name]
+    wrong = [torch.zeros([2 * n for n in t.shape], dtype=t.dtype)[tuple([slice(None, None, 2)] * t.dim())]]
+    if t.dim() > 1:
+        wrong.append(torch.zeros(t.transpose(0, 1).shape, dtype=t.dtype).transpose(0, 1))
+    if t.dim() == 3:
+        wrong.append(torch.zeros((t.shape[0], D, t.shape[1]), dtype=t.dtype).transpose(1, 2))
+        wrong.append(torch.zeros((t.shape[1], t.shape[0], D), dtype=t.dtype))   # heads before tokens
+    if t.dim() == 4:   # tokens before heads
+        wrong.append(torch.zeros((PAGES, PAGE, HKV, D), dtype=t.dtype))
+        wrong.append(torch.zeros((PAGES, PAGE, HKV, D), dtype=t.dtype).transpose(1, 2))
+    if name in ("q", "k", "v"):
+        wrong.append(t.contiguous())
+    if name in ("q_rot", "k_rot", "out"):
+        wrong.append(torch.zeros((t.shape[0], 12, D), dtype=t.dtype)[:, :t.shape[1]])
+    for w in wrong:
+        with pytest.raises(R.ReattError) as e:
+            call_with(R, call, dict(x, **{name: w}))
+        assert e.value.code == R.EINVAL, (tuple(w.shape), w.stride())
+    assert call_with(R, call, x) == R.OK
+
+
+def test_other_dtypes_and_small_workspaces_are_refused(R, on_host):
+    x = operands("prompt")
+    assert call_with(R, "prompt", operands("prompt", torch.float32), dtype="f32") == R.OK
+    for bad in (dict(cu=x["cu"].long()), dict(q=x["q"].float()), dict(out=x["out"].half()),
+                dict(ws=torch.zeros(256, dtype=torch.uint8))):
+        with pytest.raises(R.ReattError) as e:
+            call_with(R, "prompt", dict(x, **bad))
+        assert e.value.code == R.EINVAL
+
+
+def test_other_ways_to_hold_the_same_rows_pass(R, on_host):
+    """Flat buffers, rows without a dimension for the heads, padded buffers, tokens in two
+    dimensions, and fp32 words as a workspace."""
+    s, N = (HQ + 2 * HKV) * D, ROWS
+    x = operands("prompt")
+    row = torch.zeros((N + 5, HQ + 2 * HKV, D), dtype=torch.bfloat16)
+    need = R.reatt_paged_workspace_bytes(R.make_paged_dims(B=B, Hq=HQ, Hkv=HKV, d=D, dtype="bf16",
+                                                           N=N))
+    for ok in (dict(q=row, k=row[:, HQ:], v=row.flatten()[(HQ + HKV) * D:]),
+               dict(q=row.flatten(1)[:, :HQ * D], out=torch.zeros(N * HQ * D, dtype=torch.bfloat16)),
+               dict(q=row[:N].view(4, 5, HQ + 2 * HKV, D)[:, :, :HQ],
+                    out=torch.zeros((4, 5, HQ * D), dtype=torch.bfloat16)),
+               dict(cu=torch.zeros(B + 9, dtype=torch.int32)),
+               dict(ws=torch.zeros(need // 4, dtype=torch.float32))):
+        assert call_with(R, "prompt", dict(x, **ok)) == R.OK
+    # one row: the distance to the next one does not matter
+    d = R.make_paged_dims(B=1, Hq=1, Hkv=1, d=D, dtype="bf16", N=1, q_stride=s)
+    ws = torch.zeros(need, dtype=torch.uint8)
+    for q in (row[3:4, :1], row[0, 0], row[:, 0]):
+        k = torch.zeros((1, 1, D), dtype=torch.bfloat16)
+        assert R.reatt_prompt_attend(d, q, k, k, torch.zeros(2, dtype=torch.int32), k, ws,
+                                     stream=0) == R.OK

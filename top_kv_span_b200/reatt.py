@@ -8,6 +8,8 @@ the stream defaults to torch's current stream.  Missing library -> ImportError
 from __future__ import annotations
 
 import ctypes
+import functools
+import math
 import os
 
 import torch
@@ -311,23 +313,120 @@ def make_paged_dims(B, Hq, Hkv, d, dtype, N, page=1, max_pages=1, n_pages=1, rop
                             int(v_stride), int(q_rot_stride), int(k_rot_stride), float(rope_base))
 
 
-def _paged_args(where, code, data, ints, ws):
-    """Device addresses of a paged call's tensors: data, ints, ws.  What the library
-    cannot see is checked on the way: each tensor lives on the current device and has
-    the dtype of the dims (int32 for lengths and tables).  Addresses (int) and None
-    pass."""
-    want, dev, out = (torch.bfloat16 if code == BF16 else torch.float32), None, []
-    for group, dt in ((data, want), (ints, torch.int32), ((ws,), None)):
-        for t in group:
+def _rows_fit(shape, strides, N, H, d, stride) -> bool:
+    """Whether a tensor of this shape and these strides holds N packed rows of H heads of
+    d elements, dense, that lie `stride` elements apart.  The inner dimensions make up a
+    row; the outer ones, together, are the rows.  A flat buffer only has to be long
+    enough."""
+    width = H * d
+    if N == 0:
+        return True
+    if len(shape) < 2:
+        return len(shape) == 1 and (strides[0] == 1 or shape[0] == 1) and \
+            shape[0] >= (N - 1) * stride + width
+    held, rows = 1, 0
+    for size, step in zip(reversed(shape), reversed(strides)):
+        if size == 1:
+            continue
+        if not rows and step == held and held * size <= stride:
+            held *= size
+        elif step == stride * (rows or 1):
+            rows = (rows or 1) * size
+        elif N == 1:     # what lies beyond the one row does not matter
+            break
+        else:
+            return False
+    return held >= width and (rows or 1) >= N
+
+
+def _dense_fit(shape, strides, *want) -> bool:
+    """Whether a tensor is dense and holds an array of the shape `want`: as many
+    dimensions with the inner ones alike, or a flat or otherwise shaped buffer that is
+    long enough."""
+    n = 1
+    for size, step in zip(reversed(shape), reversed(strides)):
+        if size != 1 and step != n:
+            return False
+        n *= size
+    return n >= math.prod(want) and (len(shape) != len(want) or tuple(shape[1:]) == want[1:])
+
+
+class _PagedPlan:
+    """What a call asks of its operands, in the order of its list: dtype, and packed rows
+    (N, H, d, stride) or a dense array's shape; of the workspace, last, its bytes.  In
+    `fitted`, the dtype, shape and strides (None: dense) with which each one last fitted."""
+
+    def __init__(self, call, d, need):
+        want = torch.bfloat16 if d.dtype == BF16 else torch.float32
+
+        def rows(H, stride):
+            return want, _rows_fit, (d.N, H, d.d, stride or H * d.d)
+
+        q, out, q_rot = rows(d.Hq, d.q_stride), rows(d.Hq, 0), rows(d.Hq, d.q_rot_stride)
+        k, v, k_rot = (rows(d.Hkv, s) for s in (d.k_stride, d.v_stride, d.k_rot_stride))
+        pages = want, _dense_fit, (d.n_pages, d.Hkv, d.page, d.d)
+        table = torch.int32, _dense_fit, (d.B, d.max_pages)
+        cu, each = (torch.int32, _dense_fit, (d.B + 1,)), (torch.int32, _dense_fit, (d.B,))
+        self.call, self.ws_bytes = call, need
+        self.operands = {
+            "reatt_paged_append": (q, k, v, cu, each, table, q_rot, k_rot, pages, pages, each),
+            "reatt_paged_decode": (q, pages, pages, table, each, out),
+            "reatt_prompt_attend": (q, k, v, cu, out)}[call]
+        self.fitted = [(None, None, None)] * (len(self.operands) + 1)
+
+    def check(self, tensors, dev):
+        for i, t in enumerate(tensors):
             if t is None or t.__class__ is int:
-                out.append(t)
                 continue
-            if dev is None and t.is_cuda:
-                dev = torch.cuda.current_device()
-            if t.get_device() != dev or (t.dtype is not dt and dt is not None):
-                raise ReattError(EINVAL, f"{where}: a tensor of {t.dtype} on {t.device}, wanted "
-                                         f"{dt or 'any dtype'} on the current CUDA device")
+            # the workspace may have any dtype
+            dt, fit, want = self.operands[i] if i < len(self.operands) else (t.dtype, None, None)
+            if t.dtype is not dt or t.get_device() != dev:
+                raise ReattError(EINVAL, f"{self.call}: a tensor of {t.dtype} on {t.device}, "
+                                         f"wanted {dt} on the current CUDA device")
+            if fit is None:
+                ok = t.is_contiguous() and t.numel() * t.element_size() >= self.ws_bytes
+                what = f"{self.ws_bytes} bytes, dense"
+            elif fit is _rows_fit:
+                ok = fit(t.shape, t.stride(), *want)
+                what = "{} rows of {} x {}, {} elements apart".format(*want)
+            else:
+                ok, what = fit(t.shape, t.stride(), *want), f"{want}, dense"
+            if not ok:
+                raise ReattError(EINVAL, f"{self.call}: a tensor of shape {tuple(t.shape)} and "
+                                         f"strides {t.stride()}, wanted {what}")
+            self.fitted[i] = (dt, t.shape, None if t.is_contiguous() else t.stride())
+
+
+@functools.lru_cache(maxsize=256)
+def _paged_plan(call, raw):
+    """The plan for dims of these bytes; None where the call itself refuses them, before it
+    looks at any address."""
+    d, need = reatt_paged_dims.from_buffer_copy(raw), ctypes.c_size_t()
+    if lib.reatt_paged_workspace_bytes(ctypes.byref(d), ctypes.byref(need)) != OK:
+        return None
+    return _PagedPlan(call, d, need.value)
+
+
+def _paged_args(call, dims, *tensors):
+    """Device addresses of a paged call's operands, its workspace last.  What the library
+    cannot see is checked on the way: each tensor lives on the current device, has its
+    dtype and holds what the dims say where they say it.  Addresses (int) and None
+    pass.  An operand of the shape and strides that last fitted in its place fits; looking
+    at all of them anew takes 10 us."""
+    plan = _paged_plan(call, bytes(dims))
+    if plan is None:
+        return [*map(_ptr, tensors)]
+    # without an initialised CUDA there is no tensor that could be on the device
+    dev, out = torch.cuda.current_device() if torch.cuda.is_initialized() else None, []
+    for t, (dt, shape, strides) in zip(tensors, plan.fitted):
+        if t is None or t.__class__ is int:
+            out.append(t)
+        elif t.dtype is dt and t.get_device() == dev and t.shape == shape and (
+                t.is_contiguous() if strides is None else t.stride() == strides):
             out.append(t.data_ptr())
+        else:
+            plan.check(tensors, dev)
+            return [*map(_ptr, tensors)]
     return out
 
 
@@ -342,9 +441,9 @@ def reatt_paged_append(dims, q, k, v, cu_seqlens, past_len, page_table, q_rot, k
                        v_pages, seq_len, ws, stream=None, check=True):
     """Append packed new tokens to the paged caches, k (and q) rotated at their
     positions; q/q_rot, k_rot and seq_len may be None."""
-    pk, pv, pkp, pvp, pq, pqr, pkr, pcu, ppast, ptab, plen, pws = _paged_args(
-        "reatt_paged_append", dims.dtype, (k, v, k_pages, v_pages, q, q_rot, k_rot),
-        (cu_seqlens, past_len, page_table, seq_len), ws)
+    pq, pk, pv, pcu, ppast, ptab, pqr, pkr, pkp, pvp, plen, pws = _paged_args(
+        "reatt_paged_append", dims, q, k, v, cu_seqlens, past_len, page_table, q_rot, k_rot,
+        k_pages, v_pages, seq_len, ws)
     rc = lib.reatt_paged_append(ctypes.byref(dims), pq, pk, pv, pcu, ppast, ptab, pqr, pkr, pkp,
                                 pvp, plen, pws, _stream(stream))
     if check:
@@ -355,8 +454,8 @@ def reatt_paged_append(dims, q, k, v, cu_seqlens, past_len, page_table, q_rot, k
 def reatt_paged_decode(dims, q, k_pages, v_pages, page_table, seq_len, out, ws, stream=None,
                        check=True):
     """Attention of one new token per sequence over its pages."""
-    pq, pkp, pvp, pout, ptab, plen, pws = _paged_args(
-        "reatt_paged_decode", dims.dtype, (q, k_pages, v_pages, out), (page_table, seq_len), ws)
+    pq, pkp, pvp, ptab, plen, pout, pws = _paged_args(
+        "reatt_paged_decode", dims, q, k_pages, v_pages, page_table, seq_len, out, ws)
     rc = lib.reatt_paged_decode(ctypes.byref(dims), pq, pkp, pvp, ptab, plen, pout, pws,
                                 _stream(stream))
     if check:
@@ -366,8 +465,8 @@ def reatt_paged_decode(dims, q, k_pages, v_pages, page_table, seq_len, out, ws, 
 
 def reatt_prompt_attend(dims, q, k, v, cu_seqlens, out, ws, stream=None, check=True):
     """Causal attention of whole prompts, packed."""
-    pq, pk, pv, pout, pcu, pws = _paged_args("reatt_prompt_attend", dims.dtype, (q, k, v, out),
-                                             (cu_seqlens,), ws)
+    pq, pk, pv, pcu, pout, pws = _paged_args("reatt_prompt_attend", dims, q, k, v,
+                                             cu_seqlens, out, ws)
     rc = lib.reatt_prompt_attend(ctypes.byref(dims), pq, pk, pv, pcu, pout, pws, _stream(stream))
     if check:
         _check(rc, "reatt_prompt_attend")

@@ -207,6 +207,40 @@ def test_decode_infinite_value_stays_infinite(R, dtype, what):
         assert torch.equal(got, clean)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_keys_without_weight_still_count(R, dtype, d):
+    """A key whose logit is -inf has weight 0, and 0 times an infinity in its V is NaN,
+    whichever keys share its warp or range; a finite V of it adds nothing."""
+    for n, none in ((200, 16), (200, 200), (2500, 1300)):
+        pool = ref.Pool([n, 60], 1, d, 16, dtype, 7)
+        q = torch.rand((2, 4, d), generator=torch.Generator().manual_seed(4)).add(0.1).to(dtype)
+        k0, v0 = pool.rows[0]
+        pool.put(0, 0, torch.full((none, 1, d), -math.inf, dtype=dtype), v0[:none])
+        dims = R.make_paged_dims(B=2, Hq=4, Hkv=1, d=d, dtype=dtype, N=2, page=16,
+                                 max_pages=pool.max_pages, n_pages=pool.n_pages)
+        ws, outs = workspace(R, dims), []
+        for _ in range(2):
+            out = torch.empty((2, 4, d), dtype=dtype, device="cuda")
+            R.reatt_paged_decode(dims, q.cuda(), pool.k.cuda(), pool.v.cuda(), pool.table.cuda(),
+                                 ints([n, 60]), out, ws)
+            outs.append(out)
+            v = v0[3:4].clone()
+            v[0, 0, 9] = math.inf
+            pool.put(0, 3, k0[3:4] * -math.inf * k0[3:4].sign(), v)
+        clean, got = outs
+        assert torch.equal(got[1], clean[1])
+        if none == n:
+            assert clean[0].isnan().all() and got[0].isnan().all()
+            continue
+        o, tol = ref.attend(q[0].unsqueeze(1), k0[none:].transpose(0, 1), v0[none:].transpose(0, 1),
+                            torch.tensor([n - none - 1]))
+        ref.check(clean[0].cpu(), o[:, 0], tol[:, 0])
+        assert got[0, :, 9].isnan().all()
+        got[0, :, 9] = clean[0, :, 9]
+        assert torch.equal(got, clean)
+
+
 # ------------------------------------------------------------------ append
 def run_append(R, Hq, Hkv, d, dtype, page, past, new, base, *, keep_k=True, in_place=False,
                fused=True, before=0, after=0, with_q=True, seed=1):

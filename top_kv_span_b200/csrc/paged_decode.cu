@@ -172,8 +172,8 @@ __device__ __forceinline__ void pd_empty(const PagedGeom &geo, const PdArgs &a)
 // write to different banks.
 constexpr int kPdPad = 4;
 
-// Joins the warps' (m, l, o) of a unit's part, which they have left in red_ml and
-// red_o, and finishes the unit or leaves the part for the join kernel.  Every thread
+// Joins the warps' (m, l, o) of a unit's part, which they have left in red_ml (l < 0:
+// none, not even a key without weight, whose V may hold an infinity or NaN) and red_o, and finishes the unit or leaves the part for the join kernel.  Every thread
 // of the CTA calls it after a barrier, and passes another one before it writes there
 // again.
 template <typename T, int D, int HB>
@@ -194,7 +194,7 @@ __device__ __forceinline__ void pd_finish(const PagedGeom &geo, const PdArgs &a,
 #pragma unroll
         for (int i = 0; i < kPdWarps; ++i) {
             const float2 ml = red_ml[i][j];
-            if (ml.y == 0.f) continue;   // no key, or no weight: its o was not left
+            if (ml.y < 0.f) continue;   // no key: its o was not left
             const float f = pd_weight(ml.x, M);
             const float4 t = *reinterpret_cast<const float4 *>(red_o + (i * HB + j) * (D + kPdPad) + c);
             L = fmaf(f, ml.y, L);
@@ -279,6 +279,7 @@ paged_decode_f32_kernel(PagedGeom geo, PdArgs a)
     load_q(cw);
     reset();
     bool begins = cw.tile == 0;   // this part of the unit starts at its first key
+    bool any = false;             // some key of the part was this warp's
     int slot = 0;
     for (int64_t i = 0; i < n; ++i) {
         stream.load();
@@ -288,6 +289,7 @@ paged_decode_f32_kernel(PagedGeom geo, PdArgs a)
         const float *vt = kt + kPdHalf / 4;
         const int key0 = cw.tile * TILE + warp * KT;
         const bool has = key0 < cw.len;   // some key of the tile is this warp's
+        any |= has;
         float x[NB];
 #pragma unroll
         for (int nb = 0; has && nb < NB; ++nb) {
@@ -363,7 +365,7 @@ paged_decode_f32_kernel(PagedGeom geo, PdArgs a)
 #pragma unroll
             for (int w = HB; w < 32; w <<= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
             __syncthreads();   // the last part's sums have been read
-            if (lane < HB) red_ml[warp][lane] = make_float2(m, l);
+            if (lane < HB) red_ml[warp][lane] = make_float2(m, any ? l : -1.f);
 #pragma unroll
             for (int j = 0; j < HB; ++j)
 #pragma unroll
@@ -373,6 +375,7 @@ paged_decode_f32_kernel(PagedGeom geo, PdArgs a)
             __syncthreads();
             pd_finish<float, D, HB>(geo, a, cw, begins, unit_end, red_ml, red_o);
             begins = true;
+            any = false;
             reset();
         }
         cw = nw;
@@ -486,6 +489,7 @@ paged_decode_bf16_kernel(PagedGeom geo, PdArgs a)
     load_q(cw);
     reset();
     bool begins = cw.tile == 0;   // this part of the unit starts at its first key
+    bool any = false;             // some key of the part was this warp's
     int slot = 0;
     for (int64_t i = 0; i < n; ++i) {
         stream.load();
@@ -494,6 +498,7 @@ paged_decode_bf16_kernel(PagedGeom geo, PdArgs a)
         const uint32_t kt = ring + uint32_t(slot) * kPdStage, vt = kt + kPdHalf;
         const int key0 = cw.tile * TILE + warp * KT;
         const bool has = key0 < cw.len;   // some key of the tile is this warp's
+        any |= has;
         float x[KG][HT][4];
         if (has) {
 #pragma unroll
@@ -612,8 +617,8 @@ paged_decode_bf16_kernel(PagedGeom geo, PdArgs a)
 #pragma unroll
                     for (int w = 4; w < 32; w <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], w);
                     const int j = 8 * t + 2 * tc + e;
-                    if (gr == 0) red_ml[warp][j] = make_float2(m[t][e], l[t][e]);
-                    if (l[t][e] == 0.f) continue;
+                    if (gr == 0) red_ml[warp][j] = make_float2(m[t][e], any ? l[t][e] : -1.f);
+                    if (!any) continue;
 #pragma unroll
                     for (int dt = 0; dt < D / 16; ++dt) {
                         red_o[(warp * HB + j) * (D + kPdPad) + dt * 16 + gr] = o[t][dt][e];
@@ -623,6 +628,7 @@ paged_decode_bf16_kernel(PagedGeom geo, PdArgs a)
             __syncthreads();
             pd_finish<uint16_t, D, HB>(geo, a, cw, begins, unit_end, red_ml, red_o);
             begins = true;
+            any = false;
             reset();
         }
         cw = nw;

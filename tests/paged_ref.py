@@ -33,7 +33,7 @@ def attend(q, k, v, last, p_step=None):
     q = q.double()
     kk = k.double().repeat_interleave(g, 0)
     vv = v.double().repeat_interleave(g, 0)
-    off = torch.arange(m) > last[:, None]
+    off = torch.arange(m, device=last.device) > last[:, None]
     x = (q @ kk.transpose(-1, -2)) / math.sqrt(d)
     x = x.masked_fill(off, -math.inf)
     p = torch.softmax(x, -1)

@@ -1,0 +1,84 @@
+"""The paged operators with as many sequences as they take: results against plain torch
+and the definition in 64 bits, and times that grow with the tokens, not with tokens times
+sequences."""
+import math
+
+import pytest
+import torch
+
+from tests import paged_ref as ref
+from tests.test_gpu_paged import BF16, F32, R, ints, starts, workspace  # noqa: F401 (R is a fixture)
+
+pytestmark = pytest.mark.gpu
+
+MOST = 65536
+
+
+def best_us(call, n=7):
+    times = []
+    for _ in range(n):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        call()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b) * 1e3)
+    return min(times)
+
+
+def random_lengths(B, most, seed):
+    return torch.randint(0, most + 1, (B,), generator=torch.Generator().manual_seed(seed)).tolist()
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("B", [256, 257, 1000, 8191, 8193, MOST])
+@pytest.mark.parametrize("most", [1, 3])
+def test_append_finds_every_token_its_sequence(R, B, most):
+    """Un-rotated rows land in the slots that the table names, wherever their sequence is
+    among the offsets; empty sequences lie in between."""
+    lens = random_lengths(B, most, B)
+    cu, N, page, Hkv, d = starts(lens, 2), sum(lens) + 5, 4, 1, 64
+    gen = torch.Generator("cuda").manual_seed(1)
+    k, v = (torch.randn((N, Hkv, d), generator=gen, device="cuda").to(BF16) for _ in range(2))
+    past = torch.randint(0, page * 2 - 3, (B,), generator=torch.Generator().manual_seed(2)).int()
+    table = torch.randperm(2 * B, generator=torch.Generator().manual_seed(3)).int().view(B, 2)
+    dims = R.make_paged_dims(B=B, Hq=1, Hkv=Hkv, d=d, dtype=BF16, N=N, page=page, max_pages=2,
+                             n_pages=2 * B)
+    ws = workspace(R, dims)
+    pools = [torch.full((2 * B, Hkv, page, d), 7.0, dtype=BF16, device="cuda") for _ in range(2)]
+    want = [p.clone() for p in pools]
+    now = torch.empty(B, dtype=torch.int32, device="cuda")
+    R.reatt_paged_append(dims, None, k, v, ints(cu), past.cuda(), table.cuda(), None, None, *pools,
+                         now, ws)
+    n = torch.tensor(lens)
+    seq = torch.repeat_interleave(torch.arange(B), n)
+    row = torch.arange(len(seq)) + cu[0]
+    pos = past[seq] + (row - torch.tensor(cu)[seq])
+    where, slot = table[seq, (pos // page).long()].long().cuda(), (pos % page).cuda()
+    for w, x in zip(want, (k, v)):
+        w[where, :, slot.long()] = x[row.cuda()]
+    torch.cuda.synchronize()
+    assert R.reatt_workspace_status(ws) == R.OK
+    assert torch.equal(pools[0], want[0]) and torch.equal(pools[1], want[1])
+    assert torch.equal(now.cpu(), past + n.int())
+
+
+def test_append_time_does_not_grow_with_the_sequences(R):
+    """65536 tokens of as many sequences or of 64: the same bytes, and about the same time
+    (ten times as much when every token's warp read all offsets)."""
+    N, Hq, Hkv, d, page = MOST, 8, 2, 64, 16
+    q, k = (torch.zeros((N, h, d), dtype=BF16, device="cuda") for h in (Hq, Hkv))
+    pools = [torch.zeros((N, Hkv, page, d), dtype=BF16, device="cuda") for _ in range(2)]
+    outs = [torch.empty_like(q), torch.empty_like(k)]
+    times = []
+    for B in (64, MOST):
+        dims = R.make_paged_dims(B=B, Hq=Hq, Hkv=Hkv, d=d, dtype=BF16, N=N, page=page,
+                                 max_pages=N // B // page + 1, n_pages=N, rope_base=1e4)
+        cu = torch.arange(B + 1, dtype=torch.int32, device="cuda") * (N // B)
+        past, now = (torch.zeros(B, dtype=torch.int32, device="cuda") for _ in range(2))
+        table = torch.arange(B * dims.max_pages, dtype=torch.int32, device="cuda").view(B, -1) % N
+        ws = workspace(R, dims)
+        times.append(best_us(lambda: R.reatt_paged_append(dims, q, k, k, cu, past, table, *outs,
+                                                          *pools, now, ws)))
+        assert R.reatt_workspace_status(ws) == R.OK
+    assert times[1] < 4 * times[0], times

@@ -82,3 +82,66 @@ def test_append_time_does_not_grow_with_the_sequences(R):
                                                           *pools, now, ws)))
         assert R.reatt_workspace_status(ws) == R.OK
     assert times[1] < 4 * times[0], times
+
+
+# ------------------------------------------------------------------ decode
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("B", [40, 300, 9001, MOST])
+def test_decode_passes_over_empty_sequences(R, dtype, B):
+    """A batch of fixed size with few live sequences, runs of empty ones of every length
+    between them, more tiles than CTAs: every live one is found, the others are zeros."""
+    Hq, Hkv, d, page = 8, 2, 64, 128
+    gen = torch.Generator().manual_seed(B)
+    gaps = [0, 0, 1, 30, 31, 32, 33, 63, 64, 65, 200, 7000]
+    live, at = [], 0
+    for g in gaps:
+        at += g
+        if at >= B:
+            break
+        live.append(at)
+        at += 1
+    live = sorted({*live, B - 1})
+    n = {b: 3000 + 100 * i for i, b in enumerate(live)}
+    n[live[1]] = 1
+    pool = ref.Pool([n[b] for b in live], Hkv, d, page, dtype, 61)
+    table = torch.full((B, pool.max_pages), -7, dtype=torch.int32)
+    table[live] = pool.table
+    lens = torch.zeros(B, dtype=torch.int32)
+    lens[live] = torch.tensor([n[b] for b in live], dtype=torch.int32)
+    q = torch.randn((B, Hq, d), generator=gen).to(dtype)
+    dims = R.make_paged_dims(B=B, Hq=Hq, Hkv=Hkv, d=d, dtype=dtype, N=B, page=page,
+                             max_pages=pool.max_pages, n_pages=pool.n_pages)
+    ws = workspace(R, dims)
+    out = torch.full((B, Hq, d), math.nan, dtype=dtype, device="cuda")
+    R.reatt_paged_decode(dims, q.cuda(), pool.k.cuda(), pool.v.cuda(), table.cuda(), lens.cuda(),
+                         out, ws)
+    torch.cuda.synchronize()
+    assert R.reatt_workspace_status(ws) == R.OK
+    got = out[live].cpu()
+    out[live] = 0
+    assert (out == 0).all()
+    for i, b in enumerate(live):
+        k, v = (x.transpose(0, 1) for x in pool.rows[i])
+        o, tol = ref.attend(q[b].unsqueeze(1), k, v, torch.tensor([n[b] - 1]))
+        ref.check(got[i], o[:, 0], tol[:, 0], f"sequence {b}")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_decode_time_does_not_grow_with_a_gap(R, dtype):
+    """Two live sequences among 65536, side by side or at either end: the same tiles, and
+    about the same time (66 times as much when the gap was walked one by one)."""
+    B, Hq, Hkv, d, page, n = MOST, 32, 8, 128, 128, 8000
+    need = -(-n // page)
+    q = torch.zeros((B, Hq, d), dtype=dtype, device="cuda")
+    pools = [torch.zeros((2 * need, Hkv, page, d), dtype=dtype, device="cuda") for _ in range(2)]
+    dims = R.make_paged_dims(B=B, Hq=Hq, Hkv=Hkv, d=d, dtype=dtype, N=B, page=page, max_pages=need,
+                             n_pages=2 * need)
+    ws, out, times = workspace(R, dims), torch.empty_like(q), []
+    table = torch.zeros((B, need), dtype=torch.int32, device="cuda")
+    for live in ([0, 1], [0, B - 1]):
+        table[live] = torch.arange(2 * need, dtype=torch.int32, device="cuda").view(2, need)
+        lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+        lens[live] = ints([n, n - 3000])   # so that some CTA's share holds the gap
+        times.append(best_us(lambda: R.reatt_paged_decode(dims, q, *pools, table, lens, out, ws)))
+        assert R.reatt_workspace_status(ws) == R.OK
+    assert times[1] < 4 * times[0], times

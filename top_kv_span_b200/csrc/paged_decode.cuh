@@ -52,20 +52,48 @@ __device__ __forceinline__ int pd_len(const PagedGeom &geo, const int32_t *lens,
     return int(n < 0 ? 0 : (n > cap ? cap : n));
 }
 
-// Position in the list of tiles.
+// For each thread its share of the sequences, `per` of them, and the first one there that
+// has a key, or B (pd_range fills it).
+__device__ __forceinline__ int (&pd_first_live())[kPdThreads]
+{
+    __shared__ int first[kPdThreads];
+    return first;
+}
+__device__ __forceinline__ int pd_share(const PagedGeom &geo) { return (geo.B + kPdThreads - 1) / kPdThreads; }
+
+// Position in the list of tiles.  A whole warp walks it together.
 struct PdWalk {
     int b, u, tile, nt, len;
+    // To sequence nb or the first one after it that has a key.  A run of empty ones (a batch
+    // of fixed size that is mostly idle) is passed over 32 lengths at a time to the end of
+    // its share, then by shares (one by one 65534 of them held a call up for 12 ms, now 0.03).
     template <int TILE>
     __device__ __forceinline__ void enter(const PagedGeom &geo, const int32_t *lens, int nb)
     {
         b = nb;
-        len = nt = 0;
-        while (b < geo.B) {
-            len = pd_len(geo, lens, b);
-            nt = (len + TILE - 1) / TILE;
-            if (nt > 0) break;
-            ++b;
+        len = b < geo.B ? pd_len(geo, lens, b) : 0;
+        if (len == 0 && b < geo.B) {
+            b = next_live(geo, lens, b);
+            len = b < geo.B ? pd_len(geo, lens, b) : 0;
         }
+        nt = (len + TILE - 1) / TILE;
+    }
+    // The first sequence behind `at` that has a key, or B.
+    __device__ __forceinline__ static int next_live(const PagedGeom &geo, const int32_t *lens, int at)
+    {
+        const int lane = threadIdx.x & 31, per = pd_share(geo), share = at / per;
+        const int end = min((share + 1) * per, geo.B);
+        int found = geo.B;
+        for (int s = at + 1; s < end && found == geo.B; s += 32) {
+            const bool live = s + lane < end && pd_len(geo, lens, s + lane) > 0;
+            const uint32_t some = __ballot_sync(0xffffffffu, live);
+            if (some) found = s + __ffs(some) - 1;
+        }
+        for (int s = share + 1; s < kPdThreads && found == geo.B; s += 32) {
+            const int first = s + lane < kPdThreads ? pd_first_live()[s + lane] : geo.B;
+            found = __reduce_min_sync(0xffffffffu, first);   // the shares ascend
+        }
+        return found;
     }
     template <int TILE>
     __device__ __forceinline__ void next(const PagedGeom &geo, const int32_t *lens, int units)
@@ -87,10 +115,16 @@ __device__ __forceinline__ int64_t pd_range(const PagedGeom &geo, const int32_t 
     __shared__ int64_t warp_sum[kPdWarps];
     __shared__ int start[3];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (geo.B + kPdThreads - 1) / kPdThreads;
+    const int per = pd_share(geo);
     const int b0 = min(tid * per, geo.B), b1 = min(b0 + per, geo.B);
     int64_t sum = 0;
-    for (int b = b0; b < b1; ++b) sum += int64_t((pd_len(geo, lens, b) + TILE - 1) / TILE) * units;
+    int first = geo.B;
+    for (int b = b0; b < b1; ++b) {
+        const int len = pd_len(geo, lens, b);
+        sum += int64_t((len + TILE - 1) / TILE) * units;
+        if (len > 0) first = min(first, b);
+    }
+    pd_first_live()[tid] = first;
     int64_t incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

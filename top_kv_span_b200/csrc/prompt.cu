@@ -43,7 +43,7 @@ template <int D>
 __global__ void __launch_bounds__(PrSmem<D>::kThreads)
 prompt_kernel(PagedGeom geo, const float *__restrict__ q, const float *__restrict__ k,
               const float *__restrict__ v, const int32_t *__restrict__ cu, float *__restrict__ out,
-              float scale)
+              float scale, const int32_t *plan)
 {
     using Sm = PrSmem<D>;
     constexpr int OC = D / 16;   // output columns of a thread, in fours 64 apart
@@ -55,7 +55,8 @@ prompt_kernel(PagedGeom geo, const float *__restrict__ q, const float *__restric
     float *ks = mine + Sm::oK, *vs = mine + Sm::oV, *ps = mine + Sm::oP;
     pdl_wait();
     if (threadIdx.x < 32) {
-        const PromptBlock r = prompt_block(geo, cu, kPrRows, blockIdx.x / geo.Hq);
+        const int i = blockIdx.x / geo.Hq;
+        const PromptBlock r = plan ? planned_block(geo, cu, plan, kPrRows, i) : prompt_block(geo, cu, kPrRows, i);
         if (threadIdx.x == 0) blk_s = r;
     }
     __syncthreads();
@@ -228,30 +229,110 @@ prompt_kernel(PagedGeom geo, const float *__restrict__ q, const float *__restric
     }
 }
 
+// The plan (prompt.cuh): one block of threads takes the sequences kPlanThreads at a time,
+// once for every power of two that occurs, with a running sum over the block.
+constexpr int kPlanThreads = 1024;
+__global__ void __launch_bounds__(kPlanThreads)
+prompt_plan_kernel(PagedGeom geo, const int32_t *__restrict__ cu, int TB, int32_t *plan)
+{
+    __shared__ uint32_t kinds;
+    __shared__ int64_t warp_sum[kPlanThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int32_t *start = plan + 2, *order = start + geo.B + 1;
+    if (tid == 0) kinds = 0;
+    pdl_wait();
+    __syncthreads();
+    auto blocks_of = [&](int b) {
+        int s, e;
+        packed_rows(cu, b, geo.N, s, e);
+        return (e - s + TB - 1) / TB;
+    };
+    uint32_t mine = 0;
+    for (int b = tid; b < geo.B; b += kPlanThreads) {
+        const int n = blocks_of(b);
+        if (n > 0) mine |= 1u << (31 - __clz(n));
+    }
+    mine = __reduce_or_sync(0xffffffffu, mine);
+    if (lane == 0) atomicOr(&kinds, mine);
+    __syncthreads();
+    int listed = 0;
+    int64_t blocks = 0;   // (offsets that overlap can have more than 32 bits hold)
+    for (uint32_t left = kinds; left;) {
+        const int kind = 31 - __clz(left);
+        left &= ~(1u << kind);
+        for (int b0 = 0; b0 < geo.B; b0 += kPlanThreads) {
+            const int b = b0 + tid, n = b < geo.B ? blocks_of(b) : 0;
+            const bool in = n > 0 && 31 - __clz(n) == kind;
+            // blocks of the listed ones up to this thread, and how many they are
+            int64_t sum = in ? n : 0;
+            int count = in;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t up = __shfl_up_sync(0xffffffffu, sum, o);
+                const int up_count = __shfl_up_sync(0xffffffffu, count, o);
+                if (lane >= o) {
+                    sum += up;
+                    count += up_count;
+                }
+            }
+            // sums are below 2^41, counts of a block of threads below 2^11
+            if (lane == 31) warp_sum[warp] = (sum << 12) | count;
+            __syncthreads();
+            int64_t before = 0, all = 0;
+            for (int w = 0; w < kPlanThreads / 32; ++w) {
+                if (w < warp) before += warp_sum[w];
+                all += warp_sum[w];
+            }
+            if (in) {
+                const int at = listed + int(before & 4095) + count - 1;
+                const int64_t x = blocks + (before >> 12) + sum - n;
+                start[at] = int32_t(x < 0x7fffffff ? x : 0x7fffffff);
+                order[at] = b;
+            }
+            listed += int(all & 4095);
+            blocks += all >> 12;
+            __syncthreads();
+        }
+    }
+    if (tid == 0) {
+        plan[0] = listed;
+        plan[1] = int32_t(blocks < 0x7fffffff ? blocks : 0x7fffffff);
+    }
+}
+
 template <int D>
 cudaError_t run(const PagedGeom &g, const void *q, const void *k, const void *v, const int32_t *cu,
-                void *out, cudaStream_t st)
+                void *out, int32_t *plan, cudaStream_t st)
 {
     const int64_t blocks = prompt_blocks(g, kPrRows) * g.Hq;
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
     auto kern = prompt_kernel<D>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          int(PrSmem<D>::kBytes));
+    if (e == cudaSuccess && plan) e = launch_prompt_plan(g, cu, kPrRows, plan, st);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(unsigned(blocks)), dim3(PrSmem<D>::kThreads), PrSmem<D>::kBytes, st, g,
                       static_cast<const float *>(q), static_cast<const float *>(k),
                       static_cast<const float *>(v), cu, static_cast<float *>(out),
-                      float(1.4426950408889634 / sqrt(double(D))));
+                      float(1.4426950408889634 / sqrt(double(D))), static_cast<const int32_t *>(plan));
 }
 
 }  // namespace
 
+size_t prompt_ws_bytes(const PagedGeom &g) { return prompt_plan_bytes(g); }
+
+cudaError_t launch_prompt_plan(const PagedGeom &g, const int32_t *cu, int TB, int32_t *plan, cudaStream_t st)
+{
+    return launch_pdl(prompt_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, g, cu, TB, plan);
+}
+
 cudaError_t launch_prompt(const PagedGeom &g, const void *q, const void *k, const void *v,
-                          const int32_t *cu, void *out, void *ws, cudaStream_t st)
+                          const int32_t *cu, void *out, void *scratch, void *ws, cudaStream_t st)
 {
     if (g.N == 0) return cudaSuccess;
-    if (g.dtype == REATT_BF16) return launch_prompt_tc(g, q, k, v, cu, out, ws, st);
-    return g.d == 128 ? run<128>(g, q, k, v, cu, out, st) : run<64>(g, q, k, v, cu, out, st);
+    int32_t *plan = prompt_plan_bytes(g) ? static_cast<int32_t *>(scratch) : nullptr;
+    if (g.dtype == REATT_BF16) return launch_prompt_tc(g, q, k, v, cu, out, plan, ws, st);
+    return g.d == 128 ? run<128>(g, q, k, v, cu, out, plan, st) : run<64>(g, q, k, v, cu, out, plan, st);
 }
 
 }  // namespace reatt

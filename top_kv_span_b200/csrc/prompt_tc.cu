@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap vmap, PagedGeom geo,
                  const int32_t *__restrict__ cu, const uint16_t *__restrict__ v,
-                 uint16_t *__restrict__ out, float scale, void *ws)
+                 uint16_t *__restrict__ out, float scale, const int32_t *plan, void *ws)
 {
     using Sm = PtSmem<D>;
     constexpr int NS = Sm::kStages, NBOX = Sm::NBOX;
@@ -291,7 +291,9 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             int i = blockIdx.x;
             for (int k = 0;; ++k) {
                 PromptBlock p{0, 0, 0, false};
-                if (i >= 0) p = prompt_block(geo, cu, TB, i / geo.Hkv);
+                if (i >= 0)
+                    p = plan ? planned_block(geo, cu, plan, TB, i / geo.Hkv)
+                             : prompt_block(geo, cu, TB, i / geo.Hkv);
                 const Block b = block_of(p, i < 0 ? 0 : i % geo.Hkv);
                 if (lane == 0) {
                     if (b.live) {
@@ -698,7 +700,7 @@ bool packed_map(CUtensorMap *mp, const void *base, int64_t N, int H, int d, int6
 
 template <int D>
 cudaError_t run(const PagedGeom &g, const void *q, const void *k, const void *v, const int32_t *cu,
-                void *out, void *ws, cudaStream_t st)
+                void *out, int32_t *plan, void *ws, cudaStream_t st)
 {
     const int TPT = kPtRows / g.g, TB = 2 * TPT;
     const int64_t blocks = prompt_blocks(g, TB) * g.Hkv;
@@ -711,18 +713,20 @@ cudaError_t run(const PagedGeom &g, const void *q, const void *k, const void *v,
     auto kern = prompt_tc_kernel<D>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          int(PtSmem<D>::kBytes));
+    if (e == cudaSuccess && plan) e = launch_prompt_plan(g, cu, TB, plan, st);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(unsigned(blocks)), dim3(kPtThreads), PtSmem<D>::kBytes, st, qm, km, vm, g,
                       cu, static_cast<const uint16_t *>(v), static_cast<uint16_t *>(out),
-                      float(1.4426950408889634 / sqrt(double(D))), ws);
+                      float(1.4426950408889634 / sqrt(double(D))), static_cast<const int32_t *>(plan), ws);
 }
 
 }  // namespace
 
 cudaError_t launch_prompt_tc(const PagedGeom &g, const void *q, const void *k, const void *v,
-                             const int32_t *cu, void *out, void *ws, cudaStream_t st)
+                             const int32_t *cu, void *out, int32_t *plan, void *ws, cudaStream_t st)
 {
-    return g.d == 128 ? run<128>(g, q, k, v, cu, out, ws, st) : run<64>(g, q, k, v, cu, out, ws, st);
+    return g.d == 128 ? run<128>(g, q, k, v, cu, out, plan, ws, st)
+                      : run<64>(g, q, k, v, cu, out, plan, ws, st);
 }
 
 }  // namespace reatt

@@ -8,6 +8,7 @@ import torch
 
 from tests import paged_ref as ref
 from tests.test_gpu_paged import BF16, F32, R, ints, starts, workspace  # noqa: F401 (R is a fixture)
+from tests.test_gpu_paged_steady import guarded, outside_is
 
 pytestmark = pytest.mark.gpu
 
@@ -211,6 +212,40 @@ def test_prompt_time_grows_with_the_sequences_not_their_square(R, dtype):
         times.append(best_us(lambda: R.reatt_prompt_attend(dims, q, k, k, cu, out, ws), 3))
         assert R.reatt_workspace_status(ws) == R.OK
     assert times[1] < 40 * times[0], times
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("B", [129, 300, 4000])
+def test_malformed_offsets_of_many_sequences(R, dtype, B):
+    """Offsets in any order, before and behind the rows too, overlapping: nothing outside
+    the rows is written, and no row of q, k or v from outside (all NaN) reaches a result."""
+    N, Hq, Hkv, d, page = 500, 4, 2, 64, 512
+    rgen = torch.Generator().manual_seed(B)
+    gen = torch.Generator("cuda").manual_seed(B)
+    rows = []
+    for h in (Hq, Hkv, Hkv):
+        _, t = guarded((N, h, d), dtype, math.nan)
+        t.copy_(torch.randn((N, h, d), generator=gen, device="cuda"))
+        rows.append(t)
+    dims = R.make_paged_dims(B=B, Hq=Hq, Hkv=Hkv, d=d, dtype=dtype, N=N, page=page, max_pages=1,
+                             n_pages=B, rope_base=1e4)
+    ws = workspace(R, dims)
+    table = torch.arange(B, dtype=torch.int32, device="cuda").view(B, 1)
+    past = torch.zeros(B, dtype=torch.int32, device="cuda")
+    for spread in (N + 50, 1 << 31, 3):
+        cu = torch.randint(-spread, spread, (B + 1,), generator=rgen).int().cuda()
+        big, out = guarded((N, Hq, d), dtype, 5.0)
+        R.reatt_prompt_attend(dims, *rows, cu, out, ws)
+        torch.cuda.synchronize()
+        assert R.reatt_workspace_status(ws) == R.OK
+        assert outside_is(big, N, 5.0) and out.isfinite().all()
+        bufs = [guarded(s, dtype, 5.0) for s in ((N, Hq, d), (N, Hkv, d), (B, Hkv, page, d),
+                                                 (B, Hkv, page, d))]
+        R.reatt_paged_append(dims, *rows, cu, past, table, *(b[1] for b in bufs), None, ws)
+        torch.cuda.synchronize()
+        R.reatt_workspace_status(ws)
+        for big, t in bufs:
+            assert outside_is(big, t.shape[0], 5.0) and t.isfinite().all()
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])

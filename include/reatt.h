@@ -314,7 +314,12 @@ REATT_API int reatt_merge_partials(const reatt_dims *dims, int32_t n_parts,
  * reatt_step serves one long un-rotated cache through a finite window.  While
  * a sequence still fits that window (T + C <= G + k*S + L + C) the method is
  * ordinary causal RoPE attention over everything cached; these calls serve
- * that case for a batch of sequences that share a pool of pages.
+ * that case for a batch of sequences that share a pool of pages.  Two things they do
+ * not do: the pages hold rotated keys, so a sequence that outgrows the window is
+ * prefilled again into the un-rotated cache of reatt_step; and several new tokens that
+ * attend to cached ones (a chunk of a prompt, a further turn) are appended by one call but
+ * attended one token at a time by reatt_paged_decode, as reatt_prompt_attend sees the
+ * packed rows of its call only.
  *
  * Layouts (dtype = dims->dtype; int32 arrays on the device)
  *   packed rows    q [N, Hq, d], k/v [N, Hkv, d]: the new tokens of all

@@ -4,16 +4,19 @@
 //
 // One pass over the keys with the running maximum and sum of the softmax; see
 // paged_decode.cuh for how the keys are dealt out and joined again.  Every K
-// and V byte is read once for all query heads of its KV head, so memory bounds
-// it.  Each warp streams its own keys of a tile through its own ring with
+// and V byte is read once for up to 16 query heads of its KV head (fp32: 8), so memory
+// bounds it; a larger group is cut into chunks that each read all keys again.  Each
+// warp streams its own keys of a tile through its own ring with
 // 16-byte asynchronous copies and never waits for the other warps until a unit
 // ends; rows past the sequence, or on a page that the table does not name, are
 // filled with zeros in shared memory, so nothing there can reach a sum.
-// One sequence of 131073 tokens, 32/8 heads of width 128 in bf16, takes 90 us, 5.95 TB/s
-// (92% of the copy bandwidth, the join and both launches included); 61 sequences of up
-// to 8K 96 us (92%); 256 of 1.5K tokens with 12/2 heads 75 us (85%).  Where units hold
-// few keys their ends bound it: 256 sequences of 31 tokens, 25 us (32 before warps
-// without keys passed a tile over and the warps' sums were joined four at a time).
+// One sequence of 131073 tokens, 32/8 heads of width 128 in bf16, takes 89 us, 6.0 TB/s
+// (93% of the copy bandwidth, the join and both launches included); 61 sequences of up
+// to 8K 96 us (92%); 256 of 1.5K tokens with 12/2 heads 76 us (84%).  By heads of a group,
+// 269 MB of keys and values of width 128: 1 to 8 heads 50 to 53 us, 9 to 16 70 us (room for
+// one CTA an SM), 32 121 us, 128 440 us; fp32 1 to 4 heads 54 us, 5 to 8 70 us, 16 123 us,
+// 128 907 us.  Where units hold few keys their ends bound it: 256 sequences of 31 tokens,
+// 32/8 heads, 22 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -173,9 +176,9 @@ __device__ __forceinline__ void pd_empty(const PagedGeom &geo, const PdArgs &a)
 constexpr int kPdPad = 4;
 
 // Joins the warps' (m, l, o) of a unit's part, which they have left in red_ml (l < 0:
-// none, not even a key without weight, whose V may hold an infinity or NaN) and red_o, and finishes the unit or leaves the part for the join kernel.  Every thread
-// of the CTA calls it after a barrier, and passes another one before it writes there
-// again.
+// none, not even a key without weight, whose V may hold an infinity or NaN) and red_o,
+// and finishes the unit or leaves the part for the join kernel.  Every thread of the CTA
+// calls it after a barrier, and passes another one before it writes there again.
 template <typename T, int D, int HB>
 __device__ __forceinline__ void pd_finish(const PagedGeom &geo, const PdArgs &a, const PdWalk &w,
                                           bool begins, bool ends, const float2 (*red_ml)[HB],
@@ -415,14 +418,15 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x)
 // the row's low three bits (no bank conflicts), S^T turns into the operand P^T by
 // 8 x 8 transposes between registers.  P stays a sum of two bf16 terms, the value cut
 // off and what that left (up to 2^-7, rounded by 2^-8 of it: together good to 2^-14, so
-// the row sum may take the fp32 value), at two products: one bf16 term makes the result's
-// error 1.1 to 1.5 times that of its own rounding and is no faster (89, 96 and 75 us; two 89, 96 and 76).  Both terms
-// are above zero where the weight is (kPdMore sees to the second), so that an infinity in
-// V stays one.  The reference maximum of a head moves only when some logit
-// exceeds it by 2^8, so most tiles need no reduction over the keys.
+// the row sum may take the fp32 value), at two products.  One bf16 term makes the result's
+// error 1.1 to 1.5 times that of its own rounding; it took 89, 96 and 75 us where two take
+// 89, 96 and 76, and for 16 heads of width 128 62 us where two take 70.  Both terms are above
+// zero where the weight is (kPdMore sees to the second), so that an infinity in V stays
+// one.  The reference maximum of a head moves only when some logit exceeds it by 2^8, so
+// most tiles need no reduction over the keys.
 // Memory bounds it, once enough warps hide the chain of one tile (paged_decode.cuh has
 // the shapes measured); the same walk on the CUDA cores took 163, 168 and 194 us where
-// this takes 90, 96 and 75.
+// this takes 89, 96 and 76.
 constexpr float kPdMove = 8.f;
 constexpr float kPdMore = 1.f / (1 << 16);   // of the weight, added to its second term
 template <int D, int HT>

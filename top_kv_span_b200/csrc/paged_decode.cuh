@@ -18,9 +18,9 @@ namespace reatt {
 
 // Five warps a CTA with two tiles in flight each, two CTAs an SM, measured best of
 // the shapes that fit (bf16, d = 128, 128K keys of 8 KV heads / 61 sequences of up to
-// 8K / 256 of 1.5K keys of 2 KV heads): 94 / 96 / 76 us; 4 warps x 3 tiles x 2 CTAs
-// 114 / 119 / 92, 3 x 2 x 3 110 / 109 / 84, 6 x 2 x 1 92 / 108 / 86, 10 x 2 x 1
-// 96 / 104 / 83, 8 x 2 x 1 112 / 131 / 100.
+// 8K / 256 of 1.5K keys of 2 KV heads): 89 / 96 / 76 us now, 94 / 96 / 76 when the others
+// were measured: 4 warps x 3 tiles x 2 CTAs 114 / 119 / 92, 3 x 2 x 3 110 / 109 / 84,
+// 6 x 2 x 1 92 / 108 / 86, 10 x 2 x 1 96 / 104 / 83, 8 x 2 x 1 112 / 131 / 100.
 constexpr int kPdWarps = 5;             // warps of a CTA; each takes its own keys of a tile
 constexpr int kPdThreads = kPdWarps * 32;
 constexpr int kPdStages = 2;            // tiles in flight per warp

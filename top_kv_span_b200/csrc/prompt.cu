@@ -3,18 +3,20 @@
 //   o_i = sum_{t <= i} softmax_t(q_i.k_t / sqrt(d)) v_t   within each sequence
 //
 // One CTA takes 32 consecutive tokens of one query head.  Its groups of four warps
-// (four of them at width 64, one at 128) walk the keys 64 at a time in turn, each with a running maximum and sum of the
-// softmax of its own, and join at the end, so that an SM works on few blocks at a time
-// and the longest one does not outlast the others.  Scores and output stay in registers
-// (4 x 4 and 4 x d/16 per thread), and both products read four elements of either
-// operand at a time from shared memory.  A group's next K tile loads during P.V and its
-// next V tile during Q.K^T.  The arithmetic is fp32 multiply-adds; what bounds it are the
-// registers' fills from shared memory, eight 16-byte loads for 64 multiply-adds of a
-// thread.  Two prompts of 4131 tokens together, 4/1 heads of width 64, take 159 us,
-// 29 TFLOP/s (one group of four warps per CTA 210 us; on the tensor cores with operands
-// split in two tf32 terms the same, at three times the error).  Width 128 leaves room
-// for two groups in one CTA or for two CTAs of one, which is faster: a prompt of 2000
-// tokens with 32/8 heads 988 us against 1102, five of 423 together 36 against 50.
+// (four of them at width 64, one at 128) walk the keys 64 at a time in turn, each with a
+// running maximum and sum of the softmax of its own, and join at the end, so that an SM
+// works on few blocks at a time and the longest one does not outlast the others.  Scores
+// and output stay in registers (4 x 4 and 4 x d/16 per thread), and both products read
+// four elements of either operand at a time from shared memory.  A group's next K tile
+// loads during P.V and its next V tile during Q.K^T.  The arithmetic is fp32
+// multiply-adds; what bounds it are the registers' fills from shared memory, eight
+// 16-byte loads for 64 multiply-adds of a
+// thread.  K and V are read anew for every query head.  Two prompts of 4131 tokens
+// together, 4/1 heads of width 64, take 154 us, 30 TFLOP/s (one group of four warps per
+// CTA 210 us; mma.sync with operands split in two tf32 terms 160 us where this then took
+// 162, at three times the error; tcgen05 was not tried).  Width 128 leaves room for two
+// groups in one CTA or for two CTAs of one, which is faster: a prompt of 2000 tokens with
+// 32/8 heads 988 us (962 now) against 1102.
 #include <cuda_runtime.h>
 #include <math.h>
 

@@ -27,9 +27,11 @@
 // next block's loads and first S run during the last steps and the stores of this one.
 // What bounds it: the exponentials, 128 x 64 a tile and step at 16 per clock and SM,
 // as long as the products take, and what the softmax warps do besides; in long runs the
-// power limit.  A prompt of 16384 tokens, 32/8 heads of width 128, takes 1.76 ms by itself
-// and 2.03 ms in a loop (1.25 and 1.08 PFLOP/s), seven prompts of 8191 tokens together
-// 128 us.  Measured and dropped, on the way there (16384 tokens, in a loop, against what
+// power limit.  A prompt of 16384 tokens, 32/8 heads of width 128, takes 1.74 ms by itself
+// and 1.99 ms in a loop (1.26 and 1.10 PFLOP/s), seven prompts of 8191 tokens together
+// 127 us: 86 steps an SM of 0.97 us, and 7 blocks, whose ends (the look over V, the wait for
+// the last product, O on its way out, while the next block's softmax waits) take about
+// 6 us each.  Measured and dropped, on the way there (16384 tokens, in a loop, against what
 // stood then): 128-key steps with one S buffer per tile, the other way to fill the 512
 // TMEM columns, which leave the chain S -> softmax -> P.V -> S open (2.22 ms, 2.01); two
 // threads per row (2.63 ms, 2.31); a quarter of the exponentials as a polynomial on the
@@ -39,8 +41,8 @@
 // summed in fp32, and so is the row sum, of the rounded values: a weight's rounding then
 // moves a row by its share of v - o, not of v (error against 64 bits of the seven prompts
 // 0.0021 -> 0.0019, the fp32 form's 0.0016; values that all tokens share come back exact).
-// Summing the unrounded values took 125 us and 1.96 ms, this 128 us and 2.03 ms (with the
-// halves widened by integer instructions 133 us and 2.13 ms).
+// Summing the unrounded values took 125 us and 1.96 ms, this then 128 us and 2.03 ms (with
+// the halves widened by integer instructions 133 us and 2.13 ms).
 //
 // Values behind the mask: a masked S is replaced before it is used, but a masked
 // P = 0 still meets its V row in the product, so in the steps that hold any
